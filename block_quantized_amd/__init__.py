@@ -2,12 +2,15 @@
 
 Argument marshalling only: every function named ``qmm_*`` forwards to the C
 function of the same name in ``libqmm.so`` (declared in ``include/qmm.h`` and
-``include/qmm_probe.h``).
+``include/qmm_probe.h`` and ``include/qmm_kv.h``).
 Device buffers may be passed as torch tensors (their ``data_ptr()`` is used)
 or as integer device addresses; ``stream`` defaults to torch's current
 stream.  The ``qmm_*`` functions return the C status code.  The helpers
 below them (``quantize_act``, ``dequantize``, ``mul_mat`` ...) allocate their
-outputs with torch and raise :class:`QmmError` on a non-zero status.
+outputs with torch and raise :class:`QmmError` on a non-zero status.  The
+key-value cache has three plain holders of tensors (:class:`KVCache`,
+:class:`KVBatch`, :class:`Rope`) and the helpers :func:`kv_append` and
+:func:`attn` on them.
 
 There is no fallback: if ``libqmm.so`` is missing, loading fails loudly.
 """
@@ -23,10 +26,34 @@ QMM_Q4_0, QMM_Q8_0, QMM_Q4_K, QMM_Q6_K, QMM_Q8_K, QMM_Q5_0 = 1, 2, 3, 4, 5, 6
 QMM_OK, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_NULL = 0, -1, -2, -3
 QMM_ERR_ALIGN, QMM_ERR_UNSUPPORTED, QMM_ERR_HIP = -4, -5, -6
 
+QMM_F32, QMM_F16, QMM_BF16 = 32, 33, 34
+QMM_ROPE_PAIRS, QMM_ROPE_HALVES = 0, 1
+
 TYPES = {"Q4_0": QMM_Q4_0, "Q8_0": QMM_Q8_0, "Q4_K": QMM_Q4_K, "Q6_K": QMM_Q6_K, "Q8_K": QMM_Q8_K,
          "Q5_0": QMM_Q5_0}
 
 _lib = None
+
+
+class qmm_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64)]
+
+
+class qmm_kv_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+                ("max_kv", ctypes.c_int64)]
+
+
+class qmm_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n_rot", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4)]
+
+
+class qmm_attn_opts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("algo", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
 
 
 class QmmError(RuntimeError):
@@ -56,6 +83,12 @@ def lib() -> ctypes.CDLL:
             "qmm_mul_mat_algo": (I, [I, P, P, P, I64, I64, I64, I, P]),
             "qmm_mul_mat_multi": (I, [I, I, P, P, P, P, I, I64, I64, P]),
             "qmm_mul_mat_choice": (I, [I, I64, I64, I64]),
+            "qmm_kv_bytes": (SZ, [I, I, I, I, I64]),
+            "qmm_rope_freqs": (I, [P, I, ctypes.c_double, ctypes.c_double, P, P]),
+            "qmm_kv_append": (I, [P, P, P, I, P, I64, P, I64, P, I64, I, P, P]),
+            "qmm_attn": (I, [P, P, P, I, P, I64, I, P, P, SZ, P]),
+            "qmm_attn_work": (SZ, [P, P, P, I, I]),
+            "qmm_attn_choice": (I, [P, P, I, I]),
             "qmm_strerror": (ctypes.c_char_p, [I]),
             "qmm_probe_read": (I, [P, I64, P, I, P]),
             "qmm_probe_mfma": (I, [I, I64, P, P]),
@@ -72,7 +105,8 @@ def lib() -> ctypes.CDLL:
 
 EXPORTED = ("qmm_block_size", "qmm_block_bytes", "qmm_row_bytes", "qmm_vec_dot_type", "qmm_quantize_act",
             "qmm_quantize", "qmm_dequantize", "qmm_mul_mat", "qmm_mul_mat_algo", "qmm_mul_mat_multi",
-            "qmm_mul_mat_choice",
+            "qmm_mul_mat_choice", "qmm_kv_bytes", "qmm_rope_freqs", "qmm_kv_append", "qmm_attn", "qmm_attn_work",
+            "qmm_attn_choice",
             "qmm_strerror", "qmm_probe_read", "qmm_probe_mfma", "qmm_probe_mfma_ops",
             "qmm_probe_mfma16", "qmm_probe_mfma16_ops")
 
@@ -144,6 +178,37 @@ def qmm_mul_mat_multi(wtype, count, W, y, M, x, x_is_f32, N, K, stream=None) -> 
     return lib().qmm_mul_mat_multi(wtype, count, Wa, ya, Ma, _ptr(x), int(bool(x_is_f32)), N, K, _stream(stream))
 
 
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def qmm_kv_bytes(t, n_kv, head_dim, page_size, n_pages) -> int:
+    return lib().qmm_kv_bytes(t, n_kv, head_dim, page_size, n_pages)
+
+
+def qmm_rope_freqs(freqs, n_rot, base, scale=1.0, factors=None, stream=None) -> int:
+    return lib().qmm_rope_freqs(_ptr(freqs), n_rot, base, scale, _ptr(factors), _stream(stream))
+
+
+def qmm_kv_append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out, stream=None) -> int:
+    """cache, batch, rope: the structures of the same C names (or None)."""
+    return lib().qmm_kv_append(_ref(cache), _ref(batch), _ref(rope), xtype, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq,
+                               n_q, _ptr(q_out), _stream(stream))
+
+
+def qmm_attn(cache, batch, opts, xtype, q, ldq, n_q, out, work, work_bytes, stream=None) -> int:
+    return lib().qmm_attn(_ref(cache), _ref(batch), _ref(opts), xtype, _ptr(q), ldq, n_q, _ptr(out), _ptr(work),
+                          work_bytes, _stream(stream))
+
+
+def qmm_attn_work(cache, batch, opts, xtype, n_q) -> int:
+    return lib().qmm_attn_work(_ref(cache), _ref(batch), _ref(opts), xtype, n_q)
+
+
+def qmm_attn_choice(cache, batch, xtype, n_q) -> int:
+    return lib().qmm_attn_choice(_ref(cache), _ref(batch), xtype, n_q)
+
+
 def qmm_probe_read(src, nbytes, sink, workgroups=0, stream=None) -> int:
     return lib().qmm_probe_read(_ptr(src), nbytes, _ptr(sink), workgroups, _stream(stream))
 
@@ -212,3 +277,202 @@ def mul_mat(wtype: int, W, xq, M: int, N: int, K: int, algo: int = 0, stream=Non
     y = torch.empty((N, M), dtype=torch.float32, device=W.device)
     _check(qmm_mul_mat_algo(wtype, W, xq, y, M, N, K, algo, stream), "qmm_mul_mat")
     return y
+
+
+# ---------------------------------------------------- the key-value cache
+
+def _refuse(code: int, what: str):
+    raise QmmError(code, what)
+
+
+def _device_of(what: str, *tensors):
+    """The one GPU that all the tensors (None left out) lie on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            _refuse(QMM_ERR_UNSUPPORTED, f"{what}: tensors have to lie on one GPU")
+        dev = t.device
+    return dev
+
+
+def _launch_on(dev, stream):
+    """(stream handle, context): allocations and launches within the context
+    belong to that stream of that device."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+        return handle, (contextlib.nullcontext() if torch.cuda.current_device() == dev.index
+                        else torch.cuda.device(dev))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        _refuse(QMM_ERR_UNSUPPORTED, "the stream belongs to another device than the tensors")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _int32(what: str, t, *shape):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        _refuse(QMM_ERR_SHAPE, f"{what}: a contiguous int32 tensor of shape {shape} is wanted")
+
+
+class KVCache:
+    """The paged cache of one layer: tensors k and v of n_pages x n_kv x
+    page_size rows (uint8 Q8_0 blocks, float16 or bfloat16; see qmm_kv.h)."""
+
+    def __init__(self, k, v, type: int, n_kv: int, head_dim: int, page_size: int):
+        page = qmm_kv_bytes(type, n_kv, head_dim, page_size, 1)
+        if not page:
+            _refuse(QMM_ERR_UNSUPPORTED, "KVCache: type, heads, head_dim or page_size")
+        size = k.numel() * k.element_size()
+        if size != v.numel() * v.element_size() or not size or size % page:
+            _refuse(QMM_ERR_SHAPE, f"KVCache: k and v have to be whole pages of {page} bytes, as many of each")
+        if not k.is_contiguous() or not v.is_contiguous():
+            _refuse(QMM_ERR_UNSUPPORTED, "KVCache: k and v have to be contiguous")
+        self.device = _device_of("KVCache", k, v)
+        self.k, self.v, self.type = k, v, type
+        self.n_kv, self.head_dim, self.page_size, self.n_pages = n_kv, head_dim, page_size, size // page
+        self.c = qmm_kv_cache(k.data_ptr(), v.data_ptr(), type, n_kv, head_dim, page_size, self.n_pages)
+
+    @classmethod
+    def allocate(cls, type: int, n_kv: int, head_dim: int, page_size: int, n_pages: int, device="cuda"):
+        """A cache of n_pages pages, contents undefined."""
+        import torch
+        if not qmm_kv_bytes(type, n_kv, head_dim, page_size, n_pages):
+            _refuse(QMM_ERR_UNSUPPORTED, "KVCache.allocate: type, heads, head_dim, page_size or n_pages")
+        dtype = {QMM_Q8_0: torch.uint8, QMM_F16: torch.float16, QMM_BF16: torch.bfloat16}[type]
+        row = qmm_row_bytes(QMM_Q8_0, head_dim) if type == QMM_Q8_0 else head_dim
+        k, v = (torch.empty((n_pages, n_kv, page_size, row), dtype=dtype, device=device) for _ in range(2))
+        return cls(k, v, type, n_kv, head_dim, page_size)
+
+
+class KVBatch:
+    """The new tokens of a batch: q_start (n_seqs + 1), kv_len (n_seqs), table
+    (n_seqs x width), int32 on the GPU, and the rows of q, k and v."""
+
+    def __init__(self, q_start, kv_len, table, n_tokens: int, max_kv: int = 0):
+        n = kv_len.numel()
+        _int32("KVBatch: kv_len", kv_len, n)
+        _int32("KVBatch: q_start", q_start, n + 1)
+        if table.dim() != 2:
+            _refuse(QMM_ERR_SHAPE, "KVBatch: table has to be n_seqs x width")
+        _int32("KVBatch: table", table, n, table.shape[1])
+        self.device = _device_of("KVBatch", q_start, kv_len, table)
+        self.q_start, self.kv_len, self.table, self.n_tokens = q_start, kv_len, table, n_tokens
+        self.c = qmm_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n, table.shape[1], n_tokens,
+                              max_kv)
+
+
+class Rope:
+    """The rotation of positions: freqs (float64, n_rot / 2, from
+    :func:`rope_freqs`), the pairing, and pos (int32, axes x tokens, or None
+    for the index in the sequence) with the pairs of each axis."""
+
+    def __init__(self, freqs, pairing: int, pos=None, sections=None):
+        import torch
+        if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() != 1:
+            _refuse(QMM_ERR_SHAPE, "Rope: freqs has to be a contiguous float64 vector")
+        axes = len(sections) if sections is not None else 1
+        if not 1 <= axes <= 4:
+            _refuse(QMM_ERR_SHAPE, "Rope: 1 to 4 axes")
+        if pos is not None:
+            if pos.dim() == 1:
+                pos = pos[None]
+            _int32("Rope: pos", pos, axes, pos.shape[1])
+        self.device = _device_of("Rope", freqs, pos)
+        self.freqs, self.pos = freqs, pos
+        parts = list(sections if sections is not None else []) + [0] * 4
+        self.c = qmm_rope(freqs.data_ptr(), _ptr(pos), 2 * freqs.numel(), pairing, axes,
+                          (ctypes.c_int32 * 4)(*parts[:4]))
+
+
+def rope_freqs(n_rot: int, base: float, scale: float = 1.0, factors=None, device="cuda", stream=None):
+    """The angles per position of n_rot / 2 pairs, float64."""
+    import torch
+    dev = torch.device(device if factors is None else factors.device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if factors is not None and (factors.dtype != torch.float32 or factors.numel() != n_rot // 2
+                                or not factors.is_contiguous()):
+        _refuse(QMM_ERR_SHAPE, "rope_freqs: factors have to be n_rot / 2 contiguous float32 values")
+    handle, where = _launch_on(dev, stream)
+    with where:
+        freqs = torch.empty(max(n_rot // 2, 1), dtype=torch.float64, device=dev)
+        _check(qmm_rope_freqs(freqs, n_rot, base, scale, factors, handle), "qmm_rope_freqs")
+    return freqs
+
+
+def _heads(what: str, x, n_tokens: int, heads, head_dim: int):
+    """Checks a (tokens, heads, head_dim) activation, whose token rows may be
+    apart, and gives that distance."""
+    if x.dim() != 3 or x.shape[0] != n_tokens or x.shape[2] != head_dim or (heads is not None and x.shape[1] != heads):
+        _refuse(QMM_ERR_SHAPE, f"{what}: {n_tokens} x {'heads' if heads is None else heads} x {head_dim} is wanted")
+    if x.stride(2) != 1 or (x.stride(1) != head_dim and x.shape[1] != 1):
+        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: the heads of a token have to lie one after another")
+    return x.stride(0) if n_tokens > 1 else x.shape[1] * head_dim
+
+
+def _xtype(what: str, *xs):
+    import torch
+    dtype = xs[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16) or any(x is not None and x.dtype != dtype for x in xs):
+        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: activations have to be all float32 or all bfloat16")
+    return QMM_F32 if dtype == torch.float32 else QMM_BF16
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=None, stream=None):
+    """Stores k (rotated) and v (tokens, n_kv, head_dim) in the cache, and
+    returns q (tokens, n_q, head_dim) rotated, in q_out if given."""
+    import torch
+    dev = _device_of("kv_append", cache.k, batch.table, k, v, q, q_out, None if rope is None else rope.freqs)
+    N, D = batch.n_tokens, cache.head_dim
+    ldk, ldv = (_heads("kv_append", x, N, cache.n_kv, D) for x in (k, v))
+    n_q = ldq = 0
+    if q is None:
+        if q_out is not None:
+            _refuse(QMM_ERR_NULL, "kv_append: q_out without q")
+    else:
+        ldq, n_q = _heads("kv_append: q", q, N, None, D), q.shape[1]
+        if q_out is not None and (q_out.shape != q.shape or not q_out.is_contiguous()):
+            _refuse(QMM_ERR_SHAPE, "kv_append: q_out has to be contiguous and of q's shape")
+    if rope is not None and rope.pos is not None and rope.pos.shape[1] != N:
+        _refuse(QMM_ERR_SHAPE, "kv_append: pos has to name a position for every token")
+    xtype = _xtype("kv_append", k, v, q, q_out)
+    handle, where = _launch_on(dev, stream)
+    with where:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _check(qmm_kv_append(cache.c, batch.c, None if rope is None else rope.c, xtype, k, ldk, v, ldv, q, ldq, n_q,
+                             q_out, handle), "qmm_kv_append")
+    return q_out
+
+
+def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, window: int = 0, slopes=None,
+         prefix=None, algo: int = 0, out=None, stream=None):
+    """Attention of q (tokens, n_q, head_dim) over the cache -> (tokens, n_q,
+    head_dim), in out if given.  scale defaults to head_dim ** -0.5.  Rows of
+    no sequence are not written."""
+    import torch
+    dev = _device_of("attn", cache.k, batch.table, q, slopes, prefix, out)
+    N, D = batch.n_tokens, cache.head_dim
+    ldq, n_q = _heads("attn", q, N, None, D), q.shape[1]
+    xtype = _xtype("attn", q, out)
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
+        _refuse(QMM_ERR_SHAPE, "attn: out has to be contiguous and of q's shape")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != n_q or not slopes.is_contiguous()):
+        _refuse(QMM_ERR_SHAPE, "attn: slopes have to be one contiguous float32 value a query head")
+    if prefix is not None:
+        _int32("attn: prefix", prefix, batch.c.n_seqs)
+    opts = qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes), _ptr(prefix))
+    need = qmm_attn_work(cache.c, batch.c, opts, xtype, n_q)
+    handle, where = _launch_on(dev, stream)
+    with where:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(qmm_attn(cache.c, batch.c, opts, xtype, q, ldq, n_q, out, work, need, handle), "qmm_attn")
+    return out

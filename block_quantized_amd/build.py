@@ -28,7 +28,11 @@ UNITS = {
     # v_accvgpr_read, and register use drops enough for 2 waves per SIMD
     "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "probe.hip": [],
+    # stored cache rows are defined to the bit, as the codec's blocks are
+    "kv_append.hip": ["-ffp-contract=off"],
+    "attn_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "qmm.cpp": [],
+    "kv.cpp": [],
 }
 
 

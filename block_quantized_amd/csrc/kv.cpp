@@ -1,0 +1,251 @@
+// kv.cpp — the C ABI of the key-value cache (qmm_kv.h): argument validation,
+// the choice of kernels and splits, then dispatch.  As in qmm.cpp every check
+// runs before anything is enqueued, and nothing allocates, copies or
+// synchronizes.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "kv_internal.h"
+
+using namespace qmm;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 23;     // tokens + sequences: grids stay below 2^32 work-items
+constexpr int64_t kMaxLength = int64_t(1) << 30;   // tokens of a sequence
+constexpr int kMaxHeads = 4096;
+
+int hip_status(hipError_t e) { return e == hipSuccess ? QMM_OK : QMM_ERR_HIP; }
+
+int check_ptr(const void* p, unsigned align = 16) {
+    if (!p) return QMM_ERR_NULL;
+    return reinterpret_cast<uintptr_t>(p) & (align - 1) ? QMM_ERR_ALIGN : QMM_OK;
+}
+
+int check_type(int t) {
+    if (t == QMM_Q8_0 || t == QMM_F16 || t == QMM_BF16) return QMM_OK;
+    return qmm_block_size(t) || t == QMM_F32 ? QMM_ERR_UNSUPPORTED : QMM_ERR_TYPE;
+}
+
+int check_xtype(int t) {
+    if (t == QMM_F32 || t == QMM_BF16) return QMM_OK;
+    return qmm_block_size(t) || t == QMM_F16 ? QMM_ERR_UNSUPPORTED : QMM_ERR_TYPE;
+}
+
+int check_geometry(int type, int n_kv, int head_dim, int page_size, int64_t n_pages) {
+    int rc = check_type(type);
+    if (rc) return rc;
+    if (n_kv <= 0 || head_dim <= 0 || page_size <= 0 || page_size % 16 || n_pages <= 0) return QMM_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+        return QMM_ERR_UNSUPPORTED;
+    if (n_kv > kMaxHeads || page_size > kMaxLength) return QMM_ERR_SHAPE;
+    const int64_t page = (int64_t)n_kv * page_size * kv_row_bytes(type, head_dim);
+    return n_pages > INT64_MAX / 8 / page ? QMM_ERR_SHAPE : QMM_OK;
+}
+
+int check_cache(const qmm_kv_cache* c) {
+    if (!c) return QMM_ERR_NULL;
+    int rc;
+    if ((rc = check_geometry(c->type, c->n_kv, c->head_dim, c->page_size, c->n_pages))) return rc;
+    if ((rc = check_ptr(c->k)) || (rc = check_ptr(c->v))) return rc;
+    return QMM_OK;
+}
+
+int check_batch_sizes(const qmm_kv_cache* c, const qmm_kv_batch* b) {
+    if (!b) return QMM_ERR_NULL;
+    if (b->n_seqs <= 0 || b->table_width <= 0 || b->n_tokens <= 0 || b->max_kv < 0) return QMM_ERR_SHAPE;
+    if (b->n_tokens > kMaxRows || b->n_tokens + b->n_seqs > kMaxRows) return QMM_ERR_SHAPE;
+    if ((int64_t)b->table_width * c->page_size > kMaxLength) return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
+int check_batch(const qmm_kv_cache* c, const qmm_kv_batch* b) {
+    int rc;
+    if ((rc = check_batch_sizes(c, b))) return rc;
+    if ((rc = check_ptr(b->q_start, 4)) || (rc = check_ptr(b->kv_len, 4)) || (rc = check_ptr(b->table, 4))) return rc;
+    return QMM_OK;
+}
+
+int check_rows(const void* p, int64_t ld, int64_t n, int64_t heads, int head_dim) {
+    int rc;
+    if ((rc = check_ptr(p))) return rc;
+    if (ld < heads * head_dim || ld % 8 || ld > INT64_MAX / 8 / n) return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
+KvArgs kv_args(const qmm_kv_cache* c, const qmm_kv_batch* b) {
+    KvArgs a = {};
+    a.k = static_cast<uint8_t*>(c->k);
+    a.v = static_cast<uint8_t*>(c->v);
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.table = b->table;
+    a.n_pages = c->n_pages;
+    a.n_tokens = b->n_tokens;
+    a.n_seqs = b->n_seqs;
+    a.table_width = b->table_width;
+    a.page_size = c->page_size;
+    a.n_kv = c->n_kv;
+    return a;
+}
+
+int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How qmm_attn divides its work.
+struct Plan {
+    int chunk, chunks, shift, splits;
+};
+
+Plan plan_split(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
+    Plan p = {};
+    const int G = n_q / c->n_kv;
+    p.chunk = G < 16 ? G : 16;
+    p.chunks = (int)up_div(G, p.chunk);
+    while ((2 << p.shift) * p.chunk <= 16) ++p.shift;
+    // split the keys while there are fewer workgroups than two a CU, but leave
+    // each wave of a split two tiles of 32 keys
+    int64_t groups = b->n_tokens >> p.shift;
+    if (groups < b->n_seqs) groups = b->n_seqs < b->n_tokens ? b->n_seqs : b->n_tokens;
+    groups *= (int64_t)c->n_kv * p.chunks;
+    int64_t keys = (int64_t)b->table_width * c->page_size;
+    if (b->max_kv > 0 && b->max_kv < keys) keys = b->max_kv;
+    if (o->window > 0 && !o->prefix && o->window + b->n_tokens < keys) keys = o->window + b->n_tokens;
+    int64_t s = up_div(512, groups);
+    const int64_t most = up_div(keys, 256);
+    if (s > most) s = most;
+    p.splits = (int)s;
+    return p;
+}
+
+int check_opts(const qmm_attn_opts* o) {
+    if (!o) return QMM_ERR_NULL;
+    if (!isfinite(o->scale) || !isfinite(o->softcap) || o->softcap < 0 || o->window < 0) return QMM_ERR_UNSUPPORTED;
+    if (o->algo < 0 || o->algo > 1) return QMM_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(o->slopes) | reinterpret_cast<uintptr_t>(o->prefix)) & 3) return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+int check_attn_sizes(const qmm_kv_cache* c, const qmm_kv_batch* b, int xtype, int n_q) {
+    if (!c) return QMM_ERR_NULL;
+    int rc;
+    if ((rc = check_xtype(xtype))) return rc;
+    if ((rc = check_geometry(c->type, c->n_kv, c->head_dim, c->page_size, c->n_pages))) return rc;
+    if ((rc = check_batch_sizes(c, b))) return rc;
+    if (n_q <= 0 || n_q > kMaxHeads || n_q % c->n_kv) return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
+size_t work_bytes_of(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q, const Plan& p) {
+    return p.splits > 1 ? (size_t)b->n_tokens * n_q * p.splits * (c->head_dim + 2) * 4 : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qmm_kv_bytes(int type, int n_kv, int head_dim, int page_size, int64_t n_pages) {
+    if (check_geometry(type, n_kv, head_dim, page_size, n_pages)) return 0;
+    return (size_t)n_pages * n_kv * page_size * kv_row_bytes(type, head_dim);
+}
+
+int qmm_rope_freqs(double* freqs, int n_rot, double base, double scale, const float* factors, void* stream) {
+    int rc;
+    if ((rc = check_ptr(freqs, 8))) return rc;
+    if (reinterpret_cast<uintptr_t>(factors) & 3) return QMM_ERR_ALIGN;
+    if (n_rot <= 0 || n_rot % 2 || n_rot > 65536) return QMM_ERR_SHAPE;
+    if (!isfinite(base) || base <= 0 || !isfinite(scale) || scale <= 0) return QMM_ERR_UNSUPPORTED;
+    return hip_status(launch_rope_freqs(freqs, n_rot, base, scale, factors, static_cast<hipStream_t>(stream)));
+}
+
+int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_rope* rope, int xtype, const void* k,
+                  int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq, int n_q, void* q_out,
+                  void* stream) {
+    int rc;
+    if ((rc = check_xtype(xtype)) || (rc = check_cache(cache)) || (rc = check_batch(cache, batch))) return rc;
+    const int D = cache->head_dim;
+    if ((rc = check_rows(k, ldk, batch->n_tokens, cache->n_kv, D))) return rc;
+    if ((rc = check_rows(v, ldv, batch->n_tokens, cache->n_kv, D))) return rc;
+    AppendArgs a = {};
+    a.c = kv_args(cache, batch);
+    if (q || q_out) {
+        if (n_q <= 0 || n_q > kMaxHeads) return QMM_ERR_SHAPE;
+        if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, D)) || (rc = check_ptr(q_out))) return rc;
+        if (q == q_out && ldq != (int64_t)n_q * D) return QMM_ERR_SHAPE;
+        a.xq = q;
+        a.q_out = q_out;
+        a.ldq = ldq;
+        a.n_q = n_q;
+    } else if (n_q) {
+        return QMM_ERR_NULL;
+    }
+    a.xk = k;
+    a.xv = v;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    if (rope) {
+        if ((rc = check_ptr(rope->freqs, 8))) return rc;
+        if (reinterpret_cast<uintptr_t>(rope->pos) & 3) return QMM_ERR_ALIGN;
+        if (rope->n_rot <= 0 || rope->n_rot % 2 || rope->n_rot > D) return QMM_ERR_SHAPE;
+        if (rope->pairing != QMM_ROPE_PAIRS && rope->pairing != QMM_ROPE_HALVES) return QMM_ERR_UNSUPPORTED;
+        if (rope->n_axes < 1 || rope->n_axes > 4) return QMM_ERR_SHAPE;
+        a.freqs = rope->freqs;
+        a.pos = rope->pos;
+        a.n_rot = rope->n_rot;
+        a.pairing = rope->pairing;
+        int at = 0;
+        for (int i = 0; i < 3; ++i) a.bounds[i] = INT_MAX;
+        if (rope->n_axes > 1) {
+            for (int i = 0; i < rope->n_axes; ++i) {
+                if (rope->sections[i] < 0 || rope->sections[i] > D) return QMM_ERR_SHAPE;
+                at += rope->sections[i];
+                if (i + 1 < rope->n_axes) a.bounds[i] = at;
+            }
+            if (at != rope->n_rot / 2) return QMM_ERR_SHAPE;
+        }
+    }
+    return hip_status(launch_kv_append(cache->type, D, xtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q) {
+    return check_attn_sizes(cache, batch, xtype, n_q) ? 0 : 1;
+}
+
+size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
+                     int n_q) {
+    if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
+    return work_bytes_of(cache, batch, n_q, plan_split(cache, batch, opts, n_q));
+}
+
+int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,
+             int64_t ldq, int n_q, void* out, void* work, size_t work_bytes, void* stream) {
+    int rc;
+    if ((rc = check_xtype(xtype)) || (rc = check_cache(cache)) || (rc = check_batch(cache, batch))) return rc;
+    if ((rc = check_attn_sizes(cache, batch, xtype, n_q)) || (rc = check_opts(opts))) return rc;
+    if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, cache->head_dim)) || (rc = check_ptr(out))) return rc;
+    const Plan p = plan_split(cache, batch, opts, n_q);
+    const size_t need = work_bytes_of(cache, batch, n_q, p);
+    if (need) {
+        if ((rc = check_ptr(work))) return rc;
+        if (work_bytes < need) return QMM_ERR_SHAPE;
+    }
+    AttnArgs a = {};
+    a.c = kv_args(cache, batch);
+    a.q = q;
+    a.out = out;
+    a.work = static_cast<float*>(work);
+    a.slopes = opts->slopes;
+    a.prefix = opts->prefix;
+    a.ldq = ldq;
+    a.scale = opts->scale;
+    a.softcap = opts->softcap;
+    a.n_q = n_q;
+    a.window = opts->window;
+    a.splits = p.splits;
+    a.tile_shift = p.shift;
+    a.chunk = p.chunk;
+    a.chunks = p.chunks;
+    return hip_status(launch_attn_split(cache->type, cache->head_dim, xtype, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
