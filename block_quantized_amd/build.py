@@ -30,7 +30,9 @@ UNITS = {
     "probe.hip": [],
     # stored cache rows are defined to the bit, as the codec's blocks are
     "kv_append.hip": ["-ffp-contract=off"],
-    "attn_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+       for kind in ("split", "tile") for cache in ("q8_0", "f16", "bf16")},
+    "attn_join.hip": [],
     "qmm.cpp": [],
     "kv.cpp": [],
 }

@@ -1,4 +1,4 @@
-// attn_split.hip — attention over a paged cache for few query rows a
+// attn_split.h — attention over a paged cache for few query rows a
 // sequence: the cache is read once, its length split over waves and
 // workgroups, and the parts joined.
 //
@@ -27,6 +27,8 @@
 // The running maximum of a row is raised only when a score is above it by
 // more than 2^7: p may reach 2^7, which costs fp32 sums nothing and saves the
 // cross-lane maximum and the rescaling for almost every tile.
+#pragma once
+
 #include "attn_common.h"
 
 namespace qmm {
@@ -370,45 +372,13 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
     }
 }
 
-// Joins the splits of one row and head: D / 4 lanes.
-template <int D, bool XB>
-__global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
-    const int64_t row = blockIdx.x;
-    // rows of no sequence have no parts
-    const int t = (int)(row / a.n_q);
-    if (t < a.c.q_start[0] || t >= clamp_row(a.c.q_start[a.c.n_seqs], a.c.n_tokens)) return;
-    const float* ml = a.work + a.c.n_tokens * a.n_q * a.splits * D + 2 * row * a.splits;
-    const int e = 4 * threadIdx.x;
-    if (e >= D) return;
-    float top = -INFINITY;
-    for (int z = 0; z < a.splits; ++z) top = fmaxf(top, ml[2 * z]);
-    f4v sum = {0.f, 0.f, 0.f, 0.f};
-    float den = 0.f;
-    for (int z = 0; z < a.splits; ++z) {
-        const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * z] - top);
-        den += f * ml[2 * z + 1];
-        sum += f * *reinterpret_cast<const f4v*>(a.work + (row * a.splits + z) * D + e);
-    }
-    const float inv = den > 0.f ? 1.0f / den : den == 0.f ? 0.f : den;
-    sum *= inv;
-    if constexpr (XB) {
-        bf2v x, y;
-        x.x = (__bf16)sum[0], x.y = (__bf16)sum[1], y.x = (__bf16)sum[2], y.y = (__bf16)sum[3];
-        uint2 w;
-        w.x = __builtin_bit_cast(uint32_t, x), w.y = __builtin_bit_cast(uint32_t, y);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + e) = w;
-    } else {
-        *reinterpret_cast<f4v*>(static_cast<float*>(a.out) + row * D + e) = sum;
-    }
-}
-
 template <int CT, int NB, bool XB>
 hipError_t split_typed(const AttnArgs& a, hipStream_t s) {
     const int64_t items = (a.c.n_tokens >> a.tile_shift) + a.c.n_seqs;
     const dim3 grid((unsigned)items, (unsigned)(a.c.n_kv * a.chunks), (unsigned)a.splits);
     hipError_t e = launch(attn_split_kernel<CT, NB, XB>, grid, dim3(256), 0, s, a);
     if (e != hipSuccess || a.splits == 1) return e;
-    return launch(attn_join_kernel<32 * NB, XB>, dim3((unsigned)(a.c.n_tokens * a.n_q)), dim3(64), 0, s, a);
+    return launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 
 template <int CT, int NB>
@@ -416,25 +386,16 @@ hipError_t split_x(int xtype, const AttnArgs& a, hipStream_t s) {
     return xtype == QMM_BF16 ? split_typed<CT, NB, true>(a, s) : split_typed<CT, NB, false>(a, s);
 }
 
+}  // namespace
+
 template <int CT>
-hipError_t split_dims(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+hipError_t launch_attn_split_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
     case 64: return split_x<CT, 2>(xtype, a, s);
     case 96: return split_x<CT, 3>(xtype, a, s);
     case 128: return split_x<CT, 4>(xtype, a, s);
     case 192: return split_x<CT, 6>(xtype, a, s);
     case 256: return split_x<CT, 8>(xtype, a, s);
-    default: return hipErrorInvalidValue;
-    }
-}
-
-}  // namespace
-
-hipError_t launch_attn_split(int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    switch (type) {
-    case QMM_Q8_0: return split_dims<QMM_Q8_0>(head_dim, xtype, a, s);
-    case QMM_F16: return split_dims<QMM_F16>(head_dim, xtype, a, s);
-    case QMM_BF16: return split_dims<QMM_BF16>(head_dim, xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }

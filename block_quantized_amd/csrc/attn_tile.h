@@ -1,0 +1,486 @@
+// attn_tile.h — attention over a paged cache for many query rows a
+// sequence: a workgroup takes 128 query rows (tokens x the query heads of one
+// key-value head) and walks the keys in tiles of 64, which its four waves
+// stage in LDS together and each multiplies with 32 rows.
+//
+// With 32x32x16 MFMAs, as in the split kernels:
+//   S^T = K Q^T      lane (r, h) = (lane % 32, lane / 32) gets the scores of
+//                    row r with the keys 8 i + 4 h .. + 3 of a 32-key half;
+//   O^T += V^T P^T   the keys of a 16-key step in the order the lanes hold
+//                    their scores in, so P never leaves its lane.
+// K lies in LDS as it is (rows 16 bytes apart from a multiple of the banks),
+// V transposed, a row of 64 keys a value, in that key order: both are read as
+// the MFMAs' A operands with 16-byte loads that meet no bank twice.
+//
+// A wave stages the 16 keys of its number in each tile, so where they lie in
+// the cache is one page lookup, the same for its lanes.  The next tile's
+// loads are issued before a tile is multiplied.
+//
+// Exactness: bf16 queries take one product with 16-bit P.  fp32 queries and P
+// are split into two fp16 parts (three bf16 ones for a bf16 cache), and the
+// values of Q8_0 rows, d times a code, into two fp16 parts: three products of
+// parts instead of one.  Q8_0 values are staged times a power of two, the
+// same for all of a tile, that keeps the largest below 2^15.
+#pragma once
+
+#include "attn_common.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kKeys = 64;  // keys of a tile
+
+template <bool BF>
+__device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
+    if constexpr (BF)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), c, 0,
+                                                       0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), c,
+                                                      0, 0, 0);
+}
+
+// 16-byte slot of the keys `oct` (8 in the lanes' order) in the LDS row of
+// value `dim`: an order in which neither the transposing writes (four values
+// apart) nor the operand reads (one apart) meet a bank more often than needed.
+__device__ __forceinline__ int v_slot(int dim, int oct) { return oct ^ (((dim >> 1) ^ (dim >> 4)) & 7); }
+
+// What a wave has loaded of its 16 keys of a tile.
+template <int CT, int NB>
+struct Staged {
+    static constexpr bool Q8 = CT == QMM_Q8_0;
+    static constexpr int KT = Q8 ? (NB + 3) / 4 : NB;  // tasks of a lane: a block, or 16 bytes
+    static constexpr int VT = (NB + 3) / 4;            // tasks of a lane: 8 keys x 4 values
+    uint32_t k[KT][Q8 ? 9 : 4];
+    uint32_t v[VT][Q8 ? 8 : 16];
+    uint32_t vd[VT][Q8 ? 8 : 1];
+};
+
+template <int CT, int NB, bool XB>
+__global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) void attn_tile_kernel(AttnArgs a,
+                                                                                                    int items) {
+    constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
+    constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
+    constexpr int AP = Q8 && !XB ? 2 : 1;           // parts of K and V
+    constexpr int BP = XB ? 1 : BF ? 3 : 2;         // parts of Q and P
+    constexpr int KROW = 2 * D + 16;                // bytes of a row of K in LDS
+    using St = Staged<CT, NB>;
+    __shared__ __attribute__((aligned(16))) uint8_t s_k[AP][kKeys * KROW];
+    __shared__ __attribute__((aligned(16))) uint8_t s_v[AP][D * kKeys * 2];
+    __shared__ float s_big[2][4];  // of a tile, a wave's 16 keys each: the largest |d| (Q8_0),
+    __shared__ int s_page[2][4];   // and whether they have a page
+
+    // a long sequence's last tiles see the most keys: they go first.  The
+    // heads of a tile are neighbours, so (with 8 of them) each XCD keeps to one
+    // head's keys and values.
+    const int groups = a.c.n_kv * a.chunks;
+    TileAt at;
+    if (!find_tile(a, items - 1 - (int)(blockIdx.x / groups), at)) return;
+    const int hb = blockIdx.x % groups;
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kvh = hb / a.chunks, G = a.n_q / a.c.n_kv;
+    const int head0 = kvh * G + (hb % a.chunks) * a.chunk;
+    const int heads = min(a.chunk, kvh * G + G - head0);
+    const int rows = at.tokens * heads;
+    const int mr = min(32 * wave + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
+    const int p_row = at.pos + mt;
+    // the positions of the wave's first and last row
+    const int p_first = at.pos + min(32 * wave, rows - 1) / heads, p_last = at.pos + min(32 * wave + 31, rows - 1) / heads;
+    const bool idle = 32 * wave >= rows;
+
+    // ---- the queries, as B operands: lane (r, h) holds the values 8h..8h+7 of each 16
+    u4v qf[2 * NB][BP];
+    float qs;
+    {
+        const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D + 8 * h;
+        float big = 0.f;
+        // twice over the row: the first for its largest value (the second comes from L1)
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b) {
+            if constexpr (XB) {
+                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + 16 * b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+            } else {
+                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + 16 * b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(p[0][i]), fabsf(p[1][i])));
+            }
+        }
+        big = fmaxf(big, __shfl_xor(big, 32));
+        int ex = 0;
+        frexpf(big, &ex);
+        ex = min(max(ex, -110), 126);
+        const float up = ldexpf(1.0f, 14 - ex);
+        qs = ldexpf(1.0f, ex - 14) * a.scale;
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b) {
+            float x[8];
+            if constexpr (XB) {
+                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + 16 * b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+            } else {
+                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + 16 * b);
+                const f4v u = p[0], w = p[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = u[i], x[4 + i] = w[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t part[BP];
+                split_pair<BF, BP>(x[2 * i] * up, x[2 * i + 1] * up, part);
+#pragma unroll
+                for (int k = 0; k < BP; ++k) qf[b][k][i] = part[k];
+            }
+        }
+    }
+    const bool capped = a.softcap > 0.f;
+    const float inv_cap = capped ? 1.0f / a.softcap : 0.f;
+    if (!capped) qs *= kLog2e;
+    const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
+    const int reach = a.window > 0 ? a.window : INT32_MAX;
+    const int low_last = a.window > 0 ? p_last - a.window + 1 : INT32_MIN;  // every row of the wave sees keys from here
+    const int low_first = a.window > 0 ? p_first - a.window + 1 : INT32_MIN;
+
+    // ---- the tiles of this split
+    const int n_pre = (at.pre + kKeys - 1) / kKeys;
+    const int w0 = max(n_pre, at.low / kKeys), w1 = (at.end + kKeys - 1) / kKeys;
+    const int n_tiles = n_pre + max(0, w1 - w0);
+    const int per = (n_tiles + a.splits - 1) / a.splits;
+    const int t0 = (int)blockIdx.z * per, t1 = min(n_tiles, t0 + per);
+
+    f16v o[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+    float mx = -INFINITY, mref = 0.f, l = 0.f;
+    float vlim = 0x1p-30f;  // Q8_0: a power of two that no |d| so far is above
+
+    int64_t my_row = -1;  // lane i: where the wave's 16 keys of tile i from here on begin in the cache, or -1
+    St st;
+    bool paged = false;
+    // Loads the wave's keys of tile t; `big`: the largest |d| of the tile's Q8_0 blocks that this wave holds.
+    auto fetch = [&](int t) -> float {
+        const int from = (t - t0) & 63;
+        if (from == 0) {
+            const int tt = t + lane;
+            const int64_t key = (int64_t)kKeys * (tt < n_pre ? tt : tt - n_pre + w0) + 16 * wave;
+            my_row = -1;
+            if (tt < t1 && key < at.len) {
+                const int pidx = (int)key / a.c.page_size;
+                const int pg = a.c.table[(int64_t)at.s * a.c.table_width + pidx];
+                if (pg >= 0 && pg < a.c.n_pages)
+                    my_row = ((int64_t)pg * a.c.n_kv + kvh) * a.c.page_size + ((int)key - pidx * a.c.page_size);
+            }
+        }
+        const int64_t row = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, from) |
+                                      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from) << 32);
+        const int key0 = kKeys * (t < n_pre ? t : t - n_pre + w0) + 16 * wave;
+        paged = row >= 0;
+        const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;
+        const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
+        // a key that no row sees may hold anything: it counts as 0
+        const bool all = paged & ((key0 + 16 <= at.pre) | ((key0 >= at.low) & (key0 + 16 <= at.end)));
+        auto kept = [&](int key) {
+            return paged & (((key >= at.low) & (key < at.end)) | (key < at.pre));
+        };
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < St::KT; ++i) {
+            const int task = lane + 64 * i;
+            if constexpr (Q8) {
+                if (NB % 4 == 0 || task < 16 * NB) {
+                    const int key = task / NB, blk = task % NB;
+                    const uint8_t* p = kbase + key * RB + blk * kQ8_0Bytes;
+                    const bool ok = all | kept(key0 + key);
+                    st.k[i][0] = ok ? *reinterpret_cast<const uint16_t*>(p) : 0;
+                    uint64_t w[4];
+                    __builtin_memcpy(w, p + 2, 32);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) st.k[i][1 + 2 * j] = (uint32_t)w[j], st.k[i][2 + 2 * j] = (uint32_t)(w[j] >> 32);
+                    big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+                }
+            } else {
+                const int key = task / (4 * NB), c = task % (4 * NB);
+                const u4v w = *reinterpret_cast<const u4v*>(kbase + key * RB + 16 * c);
+                const bool ok = all | kept(key0 + key);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) st.k[i][j] = ok ? w[j] : 0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < St::VT; ++i) {
+            const int task = lane + 64 * i;
+            if (NB % 4 == 0 || task < 16 * NB) {
+                const int oct = task / (8 * NB), c = task % (8 * NB);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int key = 4 * oct + (j & 3) + 2 * (j & 4);  // the lanes' order of 16 keys
+                    const bool ok = all | kept(key0 + key);
+                    if constexpr (Q8) {
+                        const uint8_t* p = vbase + key * RB + (c >> 3) * kQ8_0Bytes;
+                        st.vd[i][j] = ok ? *reinterpret_cast<const uint16_t*>(p) : 0;
+                        uint32_t w;
+                        __builtin_memcpy(&w, p + 2 + 4 * (c & 7), 4);
+                        st.v[i][j] = w;
+                        big = fmaxf(big, fabsf(h2f(st.vd[i][j])));
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vbase + key * RB + 8 * c);
+                        st.v[i][2 * j] = ok ? w.x : 0, st.v[i][2 * j + 1] = ok ? w.y : 0;
+                    }
+                }
+            }
+        }
+        return big;
+    };
+    // Writes what fetch() loaded; Q8_0 values times `inv` (a power of two).
+    auto store = [&](float inv) {
+#pragma unroll
+        for (int i = 0; i < St::KT; ++i) {
+            const int task = lane + 64 * i;
+            if constexpr (Q8) {
+                if (NB % 4 == 0 || task < 16 * NB) {
+                    const int key = 16 * wave + task / NB, blk = task % NB;
+                    const float d = h2f(st.k[i][0]) * inv;
+                    uint32_t part[16][AP];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w = st.k[i][1 + j];
+                        split_pair<false, AP>(d * (float)(int8_t)w, d * (float)(int8_t)(w >> 8), part[2 * j]);
+                        split_pair<false, AP>(d * (float)(int8_t)(w >> 16), d * (float)(int8_t)(w >> 24), part[2 * j + 1]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < AP; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<u4v*>(&s_k[k][key * KROW + 64 * blk + 16 * j]) =
+                                u4v{part[4 * j][k], part[4 * j + 1][k], part[4 * j + 2][k], part[4 * j + 3][k]};
+                }
+            } else {
+                const int key = 16 * wave + task / (4 * NB), c = task % (4 * NB);
+                *reinterpret_cast<u4v*>(&s_k[0][key * KROW + 16 * c]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < St::VT; ++i) {
+            const int task = lane + 64 * i;
+            if (NB % 4 == 0 || task < 16 * NB) {
+                const int oct = 2 * wave + task / (8 * NB), c = task % (8 * NB);
+                if constexpr (Q8) {
+                    float d[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] = h2f(st.vd[i][j]) * inv;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u4v w[AP];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t part[AP];
+                            split_pair<false, AP>(d[2 * j] * (float)(int8_t)(st.v[i][2 * j] >> (8 * e)),
+                                                  d[2 * j + 1] * (float)(int8_t)(st.v[i][2 * j + 1] >> (8 * e)), part);
+#pragma unroll
+                            for (int k = 0; k < AP; ++k) w[k][j] = part[k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < AP; ++k)
+                            *reinterpret_cast<u4v*>(&s_v[k][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w[k];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u4v w;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = __builtin_amdgcn_perm(st.v[i][4 * j + 2 + (e >> 1)], st.v[i][4 * j + (e >> 1)],
+                                                         e & 1 ? 0x07060302u : 0x05040100u);
+                        *reinterpret_cast<u4v*>(&s_v[0][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w;
+                    }
+                }
+            }
+        }
+    };
+    // Loads tile t, and tells the other waves about it before the barrier that all pass before store().
+    auto begin = [&](int t) {
+        float big = fetch(t);
+        if constexpr (Q8) {
+#pragma unroll
+            for (int k = 1; k < 64; k <<= 1) big = fmaxf(big, __shfl_xor(big, k));
+        }
+        if (lane == 0) s_big[t & 1][wave] = big, s_page[t & 1][wave] = paged;
+    };
+
+    if (t0 < t1) begin(t0);
+    for (int t = t0; t < t1; ++t) {
+        __syncthreads();  // the tile before is multiplied, and s_big of this one told
+        float tile_scale = 1.0f;
+        if constexpr (Q8) {
+            const float* b = s_big[t & 1];
+            const float big = fminf(fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])), 65504.0f);
+            if (big > vlim) {  // the same in every wave
+                int ex;
+                frexpf(big, &ex);
+                const float lim = ldexpf(1.0f, ex), down = vlim / lim;
+                vlim = lim;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) o[i] *= down;
+            }
+            tile_scale = vlim * 0x1p-8f;  // values are staged as d code / tile_scale < 2^15
+            store(0x1p8f / vlim);
+        } else {
+            store(1.0f);
+        }
+        const bool full[2] = {(s_page[t & 1][0] & s_page[t & 1][1]) != 0, (s_page[t & 1][2] & s_page[t & 1][3]) != 0};
+        const bool half[4] = {s_page[t & 1][0] != 0, s_page[t & 1][1] != 0, s_page[t & 1][2] != 0, s_page[t & 1][3] != 0};
+        __syncthreads();
+        if (t + 1 < t1) begin(t + 1);
+
+        const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int k0 = kb + 32 * u;
+            // nothing of this half for any row of the wave
+            if (idle || !((k0 < at.pre) || (k0 <= p_last && k0 < at.len && k0 + 31 >= low_first))) continue;
+            f16v s;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+            for (int ap = AP - 1; ap >= 0; --ap)
+#pragma unroll
+                for (int b = 0; b < 2 * NB; ++b) {
+                    const u4v kf = *reinterpret_cast<const u4v*>(&s_k[ap][(32 * u + r) * KROW + 32 * b + 16 * h]);
+#pragma unroll
+                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) s = mfma32<BF>(kf, qf[b][k], s);
+                }
+            const float f = Q8 ? qs * tile_scale : qs;
+            float sc[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] = s[i] * f;
+            if (capped) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[i] = a.softcap * kLog2e * tanh_fp32(sc[i] * inv_cap);
+            }
+            if (a.slopes) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sc[i] -= slope * fabsf((float)(p_row - (k0 + 8 * (i >> 2) + 4 * h + (i & 3))));
+            }
+            const bool whole =
+                full[u] && ((k0 + 32 <= at.pre) || (k0 >= low_last && k0 + 32 <= min(at.len, p_first + 1)));
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+                    const bool seen = half[2 * u + (i >> 3)] & (key < at.len) &
+                                      (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
+                    sc[i] = seen ? sc[i] : -INFINITY;
+                }
+            }
+            float big = sc[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) big = fmaxf(big, sc[i]);
+            if (__any(big > mx + 7.0f)) {
+                big = fmaxf(big, __shfl_xor(big, 32));
+                const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
+                const float down = __builtin_amdgcn_exp2f(mx - ref);
+                mx = top;
+                mref = ref - 8.0f;
+                l *= down;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) o[b] *= down;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sc[i] = __builtin_amdgcn_exp2f(sc[i] - mref);
+                l += sc[i];
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                u4v pf[BP];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t part[BP];
+                    split_pair<BF, BP>(sc[8 * kk + 2 * i], sc[8 * kk + 2 * i + 1], part);
+#pragma unroll
+                    for (int k = 0; k < BP; ++k) pf[k][i] = part[k];
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int ap = AP - 1; ap >= 0; --ap) {
+                        const int dim = 32 * b + r;
+                        const u4v vf = *reinterpret_cast<const u4v*>(
+                            &s_v[ap][dim * (2 * kKeys) + 16 * v_slot(dim, 4 * u + 2 * kk + h)]);
+#pragma unroll
+                        for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[b] = mfma32<BF>(vf, pf[k], o[b]);
+                    }
+            }
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    if (32 * wave + r >= rows) return;
+    const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
+    const float unit = Q8 ? vlim * 0x1p-8f : 1.0f;
+    if (a.splits > 1) {
+        const int64_t part = row * a.splits + blockIdx.z;
+        float* ml = a.work + a.c.n_tokens * a.n_q * a.splits * D;
+        if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f4v*>(a.work + part * D + 32 * b + 8 * i + 4 * h) =
+                    f4v{o[b][4 * i] * unit, o[b][4 * i + 1] * unit, o[b][4 * i + 2] * unit, o[b][4 * i + 3] * unit};
+        return;
+    }
+    const float inv = (l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l) * unit;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = o[b][4 * i] * inv, x1 = o[b][4 * i + 1] * inv, x2 = o[b][4 * i + 2] * inv, x3 = o[b][4 * i + 3] * inv;
+            const int64_t e = row * D + 32 * b + 8 * i + 4 * h;
+            if constexpr (XB) {
+                uint32_t w0[1], w1[1];
+                split_pair<true, 1>(x0, x1, w0);
+                split_pair<true, 1>(x2, x3, w1);
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) = make_uint2(w0[0], w1[0]);
+            } else {
+                *reinterpret_cast<f4v*>(static_cast<float*>(a.out) + e) = f4v{x0, x1, x2, x3};
+            }
+        }
+}
+
+template <int CT, int NB, bool XB>
+hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
+    const int64_t items = (a.c.n_tokens >> a.tile_shift) + a.c.n_seqs;
+    const int64_t groups = items * a.c.n_kv * a.chunks;
+    if (groups >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)groups, 1, (unsigned)a.splits), dim3(256), 0, s, a,
+                          (int)items);
+    return e != hipSuccess || a.splits == 1 ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
+}
+
+template <int CT, int NB>
+hipError_t tile_x(int xtype, const AttnArgs& a, hipStream_t s) {
+    return xtype == QMM_BF16 ? tile_typed<CT, NB, true>(a, s) : tile_typed<CT, NB, false>(a, s);
+}
+
+}  // namespace
+
+template <int CT>
+hipError_t launch_attn_tile_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+    switch (head_dim) {
+    case 64: return tile_x<CT, 2>(xtype, a, s);
+    case 96: return tile_x<CT, 3>(xtype, a, s);
+    case 128: return tile_x<CT, 4>(xtype, a, s);
+    case 192: return tile_x<CT, 6>(xtype, a, s);
+    case 256: return tile_x<CT, 8>(xtype, a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmm

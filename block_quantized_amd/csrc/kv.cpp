@@ -94,19 +94,29 @@ int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How qmm_attn divides its work.
 struct Plan {
-    int chunk, chunks, shift, splits;
+    int algo, chunk, chunks, shift, splits;
 };
 
-Plan plan_split(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
+// Tile kernels multiply 128 rows at a time, split kernels 16.
+constexpr int kTileRows = 128, kSplitRows = 16;
+
+int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q) {
+    return b->n_tokens * (n_q / c->n_kv) > (int64_t)b->n_seqs * 64 ? 2 : 1;
+}
+
+Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
     Plan p = {};
     const int G = n_q / c->n_kv;
-    p.chunk = G < 16 ? G : 16;
+    p.algo = o->algo ? o->algo : choose(c, b, n_q);
+    const int rows = p.algo == 2 ? kTileRows : kSplitRows;
+    p.chunk = G < rows ? G : rows;
     p.chunks = (int)up_div(G, p.chunk);
-    while ((2 << p.shift) * p.chunk <= 16) ++p.shift;
+    while ((2 << p.shift) * p.chunk <= rows) ++p.shift;
     // split the keys while there are fewer workgroups than two a CU, but leave
-    // each wave of a split two tiles of 32 keys
-    int64_t groups = b->n_tokens >> p.shift;
-    if (groups < b->n_seqs) groups = b->n_seqs < b->n_tokens ? b->n_seqs : b->n_tokens;
+    // each split 256 keys
+    int64_t groups = up_div(b->n_tokens, int64_t(1) << p.shift);
+    const int64_t least = b->n_seqs < b->n_tokens ? b->n_seqs : b->n_tokens;
+    if (groups < least) groups = least;
     groups *= (int64_t)c->n_kv * p.chunks;
     int64_t keys = (int64_t)b->table_width * c->page_size;
     if (b->max_kv > 0 && b->max_kv < keys) keys = b->max_kv;
@@ -121,7 +131,7 @@ Plan plan_split(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opt
 int check_opts(const qmm_attn_opts* o) {
     if (!o) return QMM_ERR_NULL;
     if (!isfinite(o->scale) || !isfinite(o->softcap) || o->softcap < 0 || o->window < 0) return QMM_ERR_UNSUPPORTED;
-    if (o->algo < 0 || o->algo > 1) return QMM_ERR_UNSUPPORTED;
+    if (o->algo < 0 || o->algo > 2) return QMM_ERR_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(o->slopes) | reinterpret_cast<uintptr_t>(o->prefix)) & 3) return QMM_ERR_ALIGN;
     return QMM_OK;
 }
@@ -208,13 +218,13 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
 }
 
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q) {
-    return check_attn_sizes(cache, batch, xtype, n_q) ? 0 : 1;
+    return check_attn_sizes(cache, batch, xtype, n_q) ? 0 : choose(cache, batch, n_q);
 }
 
 size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
                      int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
-    return work_bytes_of(cache, batch, n_q, plan_split(cache, batch, opts, n_q));
+    return work_bytes_of(cache, batch, n_q, plan(cache, batch, opts, n_q));
 }
 
 int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,
@@ -223,7 +233,7 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     if ((rc = check_xtype(xtype)) || (rc = check_cache(cache)) || (rc = check_batch(cache, batch))) return rc;
     if ((rc = check_attn_sizes(cache, batch, xtype, n_q)) || (rc = check_opts(opts))) return rc;
     if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, cache->head_dim)) || (rc = check_ptr(out))) return rc;
-    const Plan p = plan_split(cache, batch, opts, n_q);
+    const Plan p = plan(cache, batch, opts, n_q);
     const size_t need = work_bytes_of(cache, batch, n_q, p);
     if (need) {
         if ((rc = check_ptr(work))) return rc;
@@ -245,7 +255,7 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     a.tile_shift = p.shift;
     a.chunk = p.chunk;
     a.chunks = p.chunks;
-    return hip_status(launch_attn_split(cache->type, cache->head_dim, xtype, a, static_cast<hipStream_t>(stream)));
+    return hip_status(launch_attn(p.algo, cache->type, cache->head_dim, xtype, a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -71,7 +71,13 @@ __device__ __forceinline__ int find_seq(const KvArgs& c, int item, int shift, in
 
 hipError_t launch_rope_freqs(double* freqs, int n_rot, double base, double scale, const float* factors, hipStream_t s);
 hipError_t launch_kv_append(int type, int head_dim, int xtype, const AppendArgs& a, hipStream_t s);
-// Split kernels: a workgroup per 16 query rows, key-value head and split.
-hipError_t launch_attn_split(int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+// Attention by the split (1) or the tile (2) kernels; each unit of a cache
+// type instantiates its own.
+hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+template <int CT>
+hipError_t launch_attn_split_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+template <int CT>
+hipError_t launch_attn_tile_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 
 }  // namespace qmm
