@@ -280,43 +280,53 @@ def mul_mat(wtype: int, W, xq, M: int, N: int, K: int, algo: int = 0, stream=Non
 
 
 # ---------------------------------------------------- the key-value cache
+#
+# A step of a small model is launches of a few microseconds, so these helpers
+# look at each tensor once and as cheaply as torch allows.
+
+_torch = None  # torch, once a helper below has needed it
+_raw_stream = None  # device index -> handle of its current stream
+
+
+def _need_torch():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        # a tenth of a microsecond instead of the two that a Stream object takes
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _torch = torch
+    return _torch
+
 
 def _refuse(code: int, what: str):
     raise QmmError(code, what)
 
 
-def _device_of(what: str, *tensors):
-    """The one GPU that all the tensors (None left out) lie on."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or (dev is not None and t.device != dev):
-            _refuse(QMM_ERR_UNSUPPORTED, f"{what}: tensors have to lie on one GPU")
-        dev = t.device
-    return dev
+def _device_of(what: str, *tensors) -> int:
+    """The index of the one GPU that all the tensors (None left out) lie on."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) != 1 or min(devs) < 0:
+        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: tensors have to lie on one GPU")
+    return devs.pop()
 
 
-def _launch_on(dev, stream):
-    """(stream handle, context): allocations and launches within the context
+def _elsewhere(dev: int, stream):
+    """(stream handle, context) for a stream given by the caller, or another
+    device than the current one: allocations and launches within the context
     belong to that stream of that device."""
-    import contextlib
-
-    import torch
+    torch = _need_torch()
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-        return handle, (contextlib.nullcontext() if torch.cuda.current_device() == dev.index
-                        else torch.cuda.device(dev))
+        return torch.cuda.current_stream(dev).cuda_stream, torch.cuda.device(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-    if stream.device != dev:
+    if stream.device.index != dev:
         _refuse(QMM_ERR_UNSUPPORTED, "the stream belongs to another device than the tensors")
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _int32(what: str, t, *shape):
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype != _need_torch().int32 or not t.is_contiguous() or tuple(t.shape) != shape:
         _refuse(QMM_ERR_SHAPE, f"{what}: a contiguous int32 tensor of shape {shape} is wanted")
 
 
@@ -333,15 +343,16 @@ class KVCache:
             _refuse(QMM_ERR_SHAPE, f"KVCache: k and v have to be whole pages of {page} bytes, as many of each")
         if not k.is_contiguous() or not v.is_contiguous():
             _refuse(QMM_ERR_UNSUPPORTED, "KVCache: k and v have to be contiguous")
-        self.device = _device_of("KVCache", k, v)
+        self.dev = _device_of("KVCache", k, v)
         self.k, self.v, self.type = k, v, type
         self.n_kv, self.head_dim, self.page_size, self.n_pages = n_kv, head_dim, page_size, size // page
         self.c = qmm_kv_cache(k.data_ptr(), v.data_ptr(), type, n_kv, head_dim, page_size, self.n_pages)
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def allocate(cls, type: int, n_kv: int, head_dim: int, page_size: int, n_pages: int, device="cuda"):
         """A cache of n_pages pages, contents undefined."""
-        import torch
+        torch = _need_torch()
         if not qmm_kv_bytes(type, n_kv, head_dim, page_size, n_pages):
             _refuse(QMM_ERR_UNSUPPORTED, "KVCache.allocate: type, heads, head_dim, page_size or n_pages")
         dtype = {QMM_Q8_0: torch.uint8, QMM_F16: torch.float16, QMM_BF16: torch.bfloat16}[type]
@@ -361,10 +372,11 @@ class KVBatch:
         if table.dim() != 2:
             _refuse(QMM_ERR_SHAPE, "KVBatch: table has to be n_seqs x width")
         _int32("KVBatch: table", table, n, table.shape[1])
-        self.device = _device_of("KVBatch", q_start, kv_len, table)
-        self.q_start, self.kv_len, self.table, self.n_tokens = q_start, kv_len, table, n_tokens
+        self.dev = _device_of("KVBatch", q_start, kv_len, table)
+        self.q_start, self.kv_len, self.table, self.n_tokens, self.n_seqs = q_start, kv_len, table, n_tokens, n
         self.c = qmm_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n, table.shape[1], n_tokens,
                               max_kv)
+        self.ref = ctypes.byref(self.c)
 
 
 class Rope:
@@ -373,8 +385,7 @@ class Rope:
     for the index in the sequence) with the pairs of each axis."""
 
     def __init__(self, freqs, pairing: int, pos=None, sections=None):
-        import torch
-        if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() != 1:
+        if freqs.dtype != _need_torch().float64 or not freqs.is_contiguous() or freqs.dim() != 1:
             _refuse(QMM_ERR_SHAPE, "Rope: freqs has to be a contiguous float64 vector")
         axes = len(sections) if sections is not None else 1
         if not 1 <= axes <= 4:
@@ -383,71 +394,101 @@ class Rope:
             if pos.dim() == 1:
                 pos = pos[None]
             _int32("Rope: pos", pos, axes, pos.shape[1])
-        self.device = _device_of("Rope", freqs, pos)
+        self.dev = _device_of("Rope", freqs, pos)
         self.freqs, self.pos = freqs, pos
+        self.tokens = None if pos is None else pos.shape[1]
         parts = list(sections if sections is not None else []) + [0] * 4
         self.c = qmm_rope(freqs.data_ptr(), _ptr(pos), 2 * freqs.numel(), pairing, axes,
                           (ctypes.c_int32 * 4)(*parts[:4]))
+        self.ref = ctypes.byref(self.c)
 
 
 def rope_freqs(n_rot: int, base: float, scale: float = 1.0, factors=None, device="cuda", stream=None):
     """The angles per position of n_rot / 2 pairs, float64."""
-    import torch
-    dev = torch.device(device if factors is None else factors.device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
+    torch = _need_torch()
+    dev = torch.device(device) if factors is None else factors.device
+    if dev.type != "cuda":
+        _refuse(QMM_ERR_UNSUPPORTED, "rope_freqs: a GPU is wanted")
+    index = torch.cuda.current_device() if dev.index is None else dev.index
     if factors is not None and (factors.dtype != torch.float32 or factors.numel() != n_rot // 2
                                 or not factors.is_contiguous()):
         _refuse(QMM_ERR_SHAPE, "rope_freqs: factors have to be n_rot / 2 contiguous float32 values")
-    handle, where = _launch_on(dev, stream)
+    handle, where = _elsewhere(index, stream)
     with where:
-        freqs = torch.empty(max(n_rot // 2, 1), dtype=torch.float64, device=dev)
+        freqs = torch.empty(max(n_rot // 2, 1), dtype=torch.float64, device=torch.device("cuda", index))
         _check(qmm_rope_freqs(freqs, n_rot, base, scale, factors, handle), "qmm_rope_freqs")
     return freqs
 
 
-def _heads(what: str, x, n_tokens: int, heads, head_dim: int):
+def _token_rows(what: str, x, n_tokens: int, head_dim: int):
     """Checks a (tokens, heads, head_dim) activation, whose token rows may be
-    apart, and gives that distance."""
-    if x.dim() != 3 or x.shape[0] != n_tokens or x.shape[2] != head_dim or (heads is not None and x.shape[1] != heads):
-        _refuse(QMM_ERR_SHAPE, f"{what}: {n_tokens} x {'heads' if heads is None else heads} x {head_dim} is wanted")
-    if x.stride(2) != 1 or (x.stride(1) != head_dim and x.shape[1] != 1):
+    apart, and gives (heads, that distance)."""
+    shape = x.shape
+    if len(shape) == 3 and shape[0] == n_tokens and shape[2] == head_dim and x.is_contiguous():
+        return shape[1], shape[1] * head_dim
+    if len(shape) != 3 or shape[0] != n_tokens or shape[2] != head_dim:
+        _refuse(QMM_ERR_SHAPE, f"{what}: {n_tokens} x heads x {head_dim} is wanted")
+    heads = shape[1]
+    row, head, one = x.stride()
+    if one != 1 or (head != head_dim and heads != 1):
         _refuse(QMM_ERR_UNSUPPORTED, f"{what}: the heads of a token have to lie one after another")
-    return x.stride(0) if n_tokens > 1 else x.shape[1] * head_dim
+    return heads, row if n_tokens > 1 else heads * head_dim
 
 
-def _xtype(what: str, *xs):
-    import torch
-    dtype = xs[0].dtype
-    if dtype not in (torch.float32, torch.bfloat16) or any(x is not None and x.dtype != dtype for x in xs):
-        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: activations have to be all float32 or all bfloat16")
-    return QMM_F32 if dtype == torch.float32 else QMM_BF16
+def _xtype(what: str, dtype):
+    if dtype == _torch.float32:
+        return QMM_F32
+    if dtype != _torch.bfloat16:
+        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: activations have to be float32 or bfloat16")
+    return QMM_BF16
+
+
+def _new_out(x):
+    return _torch.empty_like(x, memory_format=_torch.contiguous_format)
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=None, stream=None):
     """Stores k (rotated) and v (tokens, n_kv, head_dim) in the cache, and
     returns q (tokens, n_q, head_dim) rotated, in q_out if given."""
-    import torch
-    dev = _device_of("kv_append", cache.k, batch.table, k, v, q, q_out, None if rope is None else rope.freqs)
-    N, D = batch.n_tokens, cache.head_dim
-    ldk, ldv = (_heads("kv_append", x, N, cache.n_kv, D) for x in (k, v))
+    torch = _torch or _need_torch()
+    dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, k.dtype
+    same = batch.dev == dev and k.get_device() == dev and v.get_device() == dev and v.dtype == dtype
+    h, ldk = _token_rows("kv_append: k", k, N, D)
+    h2, ldv = _token_rows("kv_append: v", v, N, D)
+    if h != cache.n_kv or h2 != cache.n_kv:
+        _refuse(QMM_ERR_SHAPE, f"kv_append: k and v have to have {cache.n_kv} heads")
     n_q = ldq = 0
-    if q is None:
-        if q_out is not None:
+    if q is not None:
+        n_q, ldq = _token_rows("kv_append: q", q, N, D)
+        same = same and q.get_device() == dev and q.dtype == dtype
+    if q_out is not None:
+        if q is None:
             _refuse(QMM_ERR_NULL, "kv_append: q_out without q")
-    else:
-        ldq, n_q = _heads("kv_append: q", q, N, None, D), q.shape[1]
-        if q_out is not None and (q_out.shape != q.shape or not q_out.is_contiguous()):
+        if q_out.shape != q.shape or not q_out.is_contiguous():
             _refuse(QMM_ERR_SHAPE, "kv_append: q_out has to be contiguous and of q's shape")
-    if rope is not None and rope.pos is not None and rope.pos.shape[1] != N:
-        _refuse(QMM_ERR_SHAPE, "kv_append: pos has to name a position for every token")
-    xtype = _xtype("kv_append", k, v, q, q_out)
-    handle, where = _launch_on(dev, stream)
-    with where:
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _check(qmm_kv_append(cache.c, batch.c, None if rope is None else rope.c, xtype, k, ldk, v, ldv, q, ldq, n_q,
-                             q_out, handle), "qmm_kv_append")
+        same = same and q_out.get_device() == dev and q_out.dtype == dtype
+    if rope is not None:
+        same = same and rope.dev == dev
+        if rope.tokens is not None and rope.tokens != N:
+            _refuse(QMM_ERR_SHAPE, "kv_append: pos has to name a position for every token")
+    if not same:
+        _refuse(QMM_ERR_UNSUPPORTED, "kv_append: tensors have to lie on one GPU and be of one type")
+    xtype = _xtype("kv_append", dtype)
+    if stream is not None or torch.cuda.current_device() != dev:
+        handle, where = _elsewhere(dev, stream)
+        with where:
+            return _append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out, handle)
+    return _append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out,
+                   _raw_stream(dev))
+
+
+def _append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out, handle):
+    if q is not None and q_out is None:
+        q_out = _new_out(q)
+    rc = lib().qmm_kv_append(cache.ref, batch.ref, None if rope is None else rope.ref, xtype, k.data_ptr(), ldk,
+                             v.data_ptr(), ldv, _ptr(q), ldq, n_q, _ptr(q_out), handle)
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_append")
     return q_out
 
 
@@ -456,23 +497,41 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
     """Attention of q (tokens, n_q, head_dim) over the cache -> (tokens, n_q,
     head_dim), in out if given.  scale defaults to head_dim ** -0.5.  Rows of
     no sequence are not written."""
-    import torch
-    dev = _device_of("attn", cache.k, batch.table, q, slopes, prefix, out)
-    N, D = batch.n_tokens, cache.head_dim
-    ldq, n_q = _heads("attn", q, N, None, D), q.shape[1]
-    xtype = _xtype("attn", q, out)
-    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
-        _refuse(QMM_ERR_SHAPE, "attn: out has to be contiguous and of q's shape")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != n_q or not slopes.is_contiguous()):
-        _refuse(QMM_ERR_SHAPE, "attn: slopes have to be one contiguous float32 value a query head")
+    torch = _torch or _need_torch()
+    dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, q.dtype
+    same = batch.dev == dev and q.get_device() == dev
+    n_q, ldq = _token_rows("attn: q", q, N, D)
+    if out is not None:
+        if out.shape != q.shape or not out.is_contiguous():
+            _refuse(QMM_ERR_SHAPE, "attn: out has to be contiguous and of q's shape")
+        same = same and out.get_device() == dev and out.dtype == dtype
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.numel() != n_q or not slopes.is_contiguous():
+            _refuse(QMM_ERR_SHAPE, "attn: slopes have to be one contiguous float32 value a query head")
+        same = same and slopes.get_device() == dev
     if prefix is not None:
-        _int32("attn: prefix", prefix, batch.c.n_seqs)
-    opts = qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes), _ptr(prefix))
-    need = qmm_attn_work(cache.c, batch.c, opts, xtype, n_q)
-    handle, where = _launch_on(dev, stream)
-    with where:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(qmm_attn(cache.c, batch.c, opts, xtype, q, ldq, n_q, out, work, need, handle), "qmm_attn")
+        _int32("attn: prefix", prefix, batch.n_seqs)
+        same = same and prefix.get_device() == dev
+    if not same:
+        _refuse(QMM_ERR_UNSUPPORTED, "attn: tensors have to lie on one GPU, and out be of q's type")
+    xtype = _xtype("attn", dtype)
+    opts = ctypes.byref(qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes),
+                                      _ptr(prefix)))
+    if stream is not None or torch.cuda.current_device() != dev:
+        handle, where = _elsewhere(dev, stream)
+        with where:
+            return _attend(cache, batch, opts, xtype, q, ldq, n_q, out, handle)
+    return _attend(cache, batch, opts, xtype, q, ldq, n_q, out, _raw_stream(dev))
+
+
+def _attend(cache, batch, opts, xtype, q, ldq, n_q, out, handle):
+    L = lib()
+    need = L.qmm_attn_work(cache.ref, batch.ref, opts, xtype, n_q)
+    if out is None:
+        out = _new_out(q)
+    work = _torch.empty(need, dtype=_torch.uint8, device=q.device) if need else None
+    rc = L.qmm_attn(cache.ref, batch.ref, opts, xtype, q.data_ptr(), ldq, n_q, out.data_ptr(), _ptr(work), need,
+                    handle)
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_attn")
     return out

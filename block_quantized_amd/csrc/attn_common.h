@@ -63,6 +63,21 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t biased, uint32_t sel) {
     return __builtin_bit_cast(uint32_t, h - off);
 }
 
+// Eight int8 codes as fp16.
+__device__ __forceinline__ u4v codes8_f16(uint2 w) {
+    const uint32_t lo = w.x ^ 0x80808080u, hi = w.y ^ 0x80808080u;
+    return u4v{codes_f16(lo, 0x04010400u), codes_f16(lo, 0x04030402u), codes_f16(hi, 0x04010400u),
+               codes_f16(hi, 0x04030402u)};
+}
+
+// Eight rows of 16 bytes in LDS, transposed: of 16 lanes, lane i points at 8
+// bytes (8-byte aligned), half i % 2 of row i / 2, and gets byte i of each row.
+__device__ __forceinline__ uint2 lds_transpose8(const uint8_t* p) {
+    typedef int i2v __attribute__((ext_vector_type(2)));
+    const i2v r = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i2v*)p);
+    return make_uint2((uint32_t)r.x, (uint32_t)r.y);
+}
+
 // tanh(x): the Taylor series (to x^11; the next term is below 4e-9 x) where
 // 1 - 2 / (e^2x + 1) would lose bits to cancellation, that form elsewhere.
 __device__ __forceinline__ float tanh_fp32(float x) {
@@ -73,7 +88,8 @@ __device__ __forceinline__ float tanh_fp32(float x) {
     p = fmaf(p, x2, 2.0f / 15.0f);
     p = fmaf(p, x2, -1.0f / 3.0f);
     const float small = fmaf(p * x2, x, x);
-    const float big = 1.0f - 2.0f / (__builtin_amdgcn_exp2f(2.0f * kLog2e * fabsf(x)) + 1.0f);
+    if (!__any(fabsf(x) >= 0.35f)) return small;
+    const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * kLog2e * fabsf(x)) + 1.0f);
     return fabsf(x) < 0.35f ? small : copysignf(big, x);
 }
 
@@ -85,28 +101,120 @@ struct TileAt {
     int end, low;               // keys any of the tokens sees: [low, end) and [0, pre)
 };
 
-// The tile `item` of the row tiles of 2^shift tokens.  Sequence s owns the
-// items from (q_start[s] >> shift) + s on: at least ceil(n / 2^shift) of them,
-// and some that are empty (false).
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int item, TileAt& t) {
-    const int sh = a.tile_shift;
-    const int s = __builtin_amdgcn_readfirstlane(find_seq(a.c, item, sh, 1, a.c.n_seqs));
-    if (s < 0) return false;
-    const int q0 = clamp_row(a.c.q_start[s], a.c.n_tokens), q1 = clamp_row(a.c.q_start[s + 1], a.c.n_tokens);
-    const int64_t first = (int64_t)(item - ((q0 >> sh) + s)) << sh;
-    if (first >= q1 - q0) return false;
-    t.s = s;
-    t.first = (int)first;
-    t.row = q0 + t.first;
-    t.tokens = min(1 << sh, q1 - q0 - t.first);
-    const int kv = max(a.c.kv_len[s], 0);
+// What a lane reads of its sequence (nothing of it is trusted further than
+// that it is some number).
+struct SeqAt {
+    int q0, q1, kv, pre;
+};
+__device__ __forceinline__ SeqAt seq_at(const AttnArgs& a, int s) {
     const int64_t room = (int64_t)a.c.table_width * a.c.page_size;
-    t.len = (int64_t)kv < room ? kv : (int)room;
-    t.pos = kv - (q1 - q0) + t.first;
-    t.pre = a.prefix ? min(max(a.prefix[s], 0), t.len) : 0;
+    SeqAt q;
+    const int32_t q0 = a.c.q_start[s], q1 = a.c.q_start[s + 1], kv = a.c.kv_len[s], pre = a.prefix ? a.prefix[s] : 0;
+    q.q0 = clamp_row(q0, a.c.n_tokens), q.q1 = clamp_row(q1, a.c.n_tokens);
+    q.kv = max(kv, 0);
+    q.pre = min(max(pre, 0), (int64_t)q.kv < room ? q.kv : (int)room);
+    return q;
+}
+
+// The row tile that begins with token `first` of sequence s.
+__device__ __forceinline__ TileAt tile_at(const AttnArgs& a, int s, const SeqAt& q, int first) {
+    TileAt t;
+    t.s = s;
+    t.first = first;
+    t.row = q.q0 + first;
+    t.tokens = min(1 << a.tile_shift, q.q1 - q.q0 - first);
+    const int64_t room = (int64_t)a.c.table_width * a.c.page_size;
+    t.len = (int64_t)q.kv < room ? q.kv : (int)room;
+    t.pos = q.kv - (q.q1 - q.q0) + first;
+    t.pre = q.pre;
     t.end = max(0, min(t.len, t.pos + t.tokens));
     t.low = a.window > 0 && t.pos >= a.window ? t.pos - a.window + 1 : 0;
-    return true;
+    return t;
+}
+
+// A work item: a row tile of a sequence, and a part of the keys it sees.
+struct Work {
+    TileAt at;
+    int split, splits;
+    int first, step;  // the row tile's first item, and from one split's to the next
+};
+
+// Work item `item`, by one wavefront; false if there are fewer.  Sequence s
+// makes ceil(tokens / 2^tile_shift) row tiles, each split in as many parts as
+// its keys fill chunks of equal size: the chunk is the keys of all row tiles
+// over a.splits, so a.splits + (number of row tiles) items hold them all, and
+// a long sequence among short ones is divided as finely as they are small
+// (64 conversations of 8k to 16k keys: 382 -> 338 us against as many splits
+// of each).  Without splits (0) a row tile is one item.  Items go split by
+// split within a sequence; `last_first` turns the row tiles around.
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, bool last_first = false) {
+    const int lane = threadIdx.x & 63, n = a.c.n_seqs;
+    SeqAt q = {};
+    unsigned tiles = 0, keys = 0;  // of the lane's sequence: row tiles, and blocks of 32 keys
+    auto look = [&](int s) {
+        tiles = keys = 0;
+        if (s >= n) return;
+        q = seq_at(a, s);
+        if (q.q1 <= q.q0) return;
+        tiles = ((q.q1 - q.q0 - 1) >> a.tile_shift) + 1;
+        const TileAt t = tile_at(a, s, q, 0);
+        const int pre = (t.pre + 31) >> 5;
+        keys = pre + max(0, ((t.len + 31) >> 5) - max(pre, t.low >> 5));
+    };
+    look(lane);
+    unsigned chunk = 0;
+    if (a.splits) {
+        double all = 0.0;
+        for (int s0 = 0; s0 < n; s0 += 64) {
+            if (n > 64) look(s0 + lane);
+            all += (double)tiles * (double)keys;
+        }
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) all += __shfl_xor(all, k);
+        chunk = max(a.least, (int)(all / (double)a.splits) + 1);
+    }
+    int base = 0;
+    for (int s0 = 0; s0 < n; s0 += 64) {
+        if (n > 64) look(s0 + lane);
+        const unsigned parts = chunk && keys ? (keys - 1) / chunk + 1 : 1;
+        int upto = (int)(tiles * parts);
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+            if (k < n) {
+                const int below = __shfl_up(upto, k);
+                upto += lane >= k ? below : 0;
+            }
+        }
+        const uint64_t over = __ballot(base + upto > item);
+        if (over) {
+            const int at = __ffsll((unsigned long long)over) - 1;
+            const int t = __builtin_amdgcn_readlane((int)tiles, at), p = __builtin_amdgcn_readlane((int)parts, at);
+            const int start = base + __builtin_amdgcn_readlane(upto, at) - t * p, i = item - start;
+            // (not so only where q_start is no batch's)
+            if (t <= 0 || i < 0 || i >= (int64_t)t * p) return false;
+            w.splits = p;
+            w.split = (int)((unsigned)i / (unsigned)t);
+            int tile = i - w.split * t;
+            w.first = start + tile;
+            w.step = t;
+            if (last_first) tile = t - 1 - tile;
+            const SeqAt u = {__builtin_amdgcn_readlane(q.q0, at), __builtin_amdgcn_readlane(q.q1, at),
+                             __builtin_amdgcn_readlane(q.kv, at), __builtin_amdgcn_readlane(q.pre, at)};
+            w.at = tile_at(a, s0 + at, u, tile << a.tile_shift);
+            return true;
+        }
+        base += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+// Where the join finds the parts of a row: part (first + z step) * slots +
+// slot for its splits z.  0 splits: the row is written already.
+struct JoinOf {
+    int first, splits, step, slot;
+};
+__device__ __forceinline__ JoinOf* join_of(const AttnArgs& a) {
+    return reinterpret_cast<JoinOf*>(a.work + a.parts * (a.head_dim + 2));
 }
 
 }  // namespace qmm

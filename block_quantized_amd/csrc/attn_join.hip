@@ -5,25 +5,47 @@
 namespace qmm {
 namespace {
 
-// Joins the splits of one row and head: D / 4 lanes.
+// Joins the splits of one row and head.  Four wavefronts take every fourth
+// split: a lane four values, so a wavefront reads 64 / (D / 4) splits at a time
+// (one of 256 values), with the splits' weights from LDS.
 template <int D, bool XB>
-__global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    constexpr int LANES = D / 4, AT = 256 / LANES;  // lanes of a split, splits at a time
     const int64_t row = blockIdx.x;
     // rows of no sequence have no parts
     const int t = (int)(row / a.n_q);
     if (t < a.c.q_start[0] || t >= clamp_row(a.c.q_start[a.c.n_seqs], a.c.n_tokens)) return;
-    const float* ml = a.work + a.c.n_tokens * a.n_q * a.splits * D + 2 * row * a.splits;
-    const int e = 4 * threadIdx.x;
-    if (e >= D) return;
+    const JoinOf j = join_of(a)[row];
+    const int64_t slots = a.parts / a.items;
+    if (j.splits <= 0 || j.first < 0 || j.step <= 0 || j.slot < 0 || j.slot >= slots ||
+        j.first + (j.splits - 1) * (int64_t)j.step >= a.items)
+        return;  // one part, or (with a batch that is none) nothing written here
+    const float* ml = a.work + a.parts * D + 2 * (j.first * slots + j.slot);
+    const float* part = a.work + (j.first * slots + j.slot) * D;
+    const int64_t step = j.step * slots;
+    const int lane = threadIdx.x & 63;
+    // every wavefront for itself: the largest maximum
     float top = -INFINITY;
-    for (int z = 0; z < a.splits; ++z) top = fmaxf(top, ml[2 * z]);
+    for (int z = lane; z < j.splits; z += 64) top = fmaxf(top, ml[2 * step * z]);
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+    const int mine = threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES);
     f4v sum = {0.f, 0.f, 0.f, 0.f};
     float den = 0.f;
-    for (int z = 0; z < a.splits; ++z) {
-        const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * z] - top);
-        den += f * ml[2 * z + 1];
-        sum += f * *reinterpret_cast<const f4v*>(a.work + (row * a.splits + z) * D + e);
+    if (mine < AT && top != -INFINITY) {
+        for (int z = mine; z < j.splits; z += AT) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * step * z] - top);
+            den += f * ml[2 * step * z + 1];
+            sum += f * *reinterpret_cast<const f4v*>(part + step * z * D + e);
+        }
     }
+    __shared__ f4v s_sum[256];
+    __shared__ float s_den[256];
+    s_sum[threadIdx.x] = sum, s_den[threadIdx.x] = den;
+    __syncthreads();
+    if (mine > 0) return;
+#pragma unroll
+    for (int z = 1; z < AT; ++z) sum += s_sum[threadIdx.x + z * LANES], den += s_den[threadIdx.x + z * LANES];
     const float inv = den > 0.f ? 1.0f / den : den == 0.f ? 0.f : den;
     sum *= inv;
     if constexpr (XB) {
@@ -40,14 +62,14 @@ __global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
 template <int D>
 hipError_t join_x(int xtype, const AttnArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.c.n_tokens * a.n_q));
-    return xtype == QMM_BF16 ? launch(attn_join_kernel<D, true>, grid, dim3(64), 0, s, a)
-                             : launch(attn_join_kernel<D, false>, grid, dim3(64), 0, s, a);
+    return xtype == QMM_BF16 ? launch(attn_join_kernel<D, true>, grid, dim3(256), 0, s, a)
+                             : launch(attn_join_kernel<D, false>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    if (a.c.n_tokens * a.n_q >= (int64_t(1) << 26)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    if (a.c.n_tokens * a.n_q >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
     switch (head_dim) {
     case 64: return join_x<64>(xtype, a, s);
     case 96: return join_x<96>(xtype, a, s);

@@ -41,43 +41,55 @@ __device__ __forceinline__ constexpr int parts_of() { return CT == QMM_BF16 ? 3 
 
 __device__ __forceinline__ uint32_t ld16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
+// Q8_0: LDS bytes of a wave's 32 keys or values, blocks and their scales.
+template <int NB>
+constexpr int kStage = 32 * 34 * NB + 64 * NB;
+
 template <int CT, int NB, bool XB>
-__global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D), PARTS = parts_of<CT>();
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
-    TileAt at;
-    if (!find_tile(a, blockIdx.x, at)) return;
+    // LDS: the queries and the waves' staging regions, then the waves' parts
+    constexpr int PARTS_BYTES = kWaves * 16 * (D + 4) * 4, Q_BYTES = NB * PARTS * 64 * 16;
+    constexpr int USED_BYTES = Q_BYTES + (Q8 ? kWaves * kStage<NB> : 0);
+    __shared__ __attribute__((aligned(16))) uint8_t smem[PARTS_BYTES > USED_BYTES ? PARTS_BYTES : USED_BYTES];
+    u4v(*s_q)[PARTS][64] = reinterpret_cast<u4v(*)[PARTS][64]>(smem);
+    const int groups = a.c.n_kv * a.chunks, item = (int)(blockIdx.x / groups), hb = blockIdx.x % groups;
+    Work w;
+    if (!find_work(a, item, w)) return;
+    const TileAt at = w.at;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kvh = blockIdx.y / a.chunks, G = a.n_q / a.c.n_kv;
-    const int head0 = kvh * G + (blockIdx.y % a.chunks) * a.chunk;  // first query head of the tile
+    const int kvh = hb / a.chunks, G = a.n_q / a.c.n_kv;
+    const int head0 = kvh * G + (hb % a.chunks) * a.chunk;  // first query head of the tile
     const int heads = min(a.chunk, kvh * G + G - head0);
     // row m of the tile: token m / heads, head m % heads
     const int rows = min(16, at.tokens * heads);
     const int mr = min(m, rows - 1), mt = mr / heads, head = head0 + mr % heads;
     const int p_row = at.pos + mt;
 
-    // ---- the queries, as B operands: lane (m, g) holds the values 8g..8g+7 of each block
-    u4v qf[NB][PARTS];
+    // ---- the queries, as B operands in LDS (the waves', one quarter of the
+    // blocks written by each): lane (m, g) holds the values 8g..8g+7 of each block
     float qs;  // what a score is multiplied by
     {
         float x[NB][8];
-        const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D + 8 * g;
+        const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D;
         float big = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            if constexpr (XB) {
-                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + 32 * b);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[b][2 * i] = bf16_lo(w[i]), x[b][2 * i + 1] = bf16_hi(w[i]);
-            } else {
-                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + 32 * b);
-                const f4v u = p[0], w = p[1];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[b][i] = u[i], x[b][4 + i] = w[i];
+            for (int i = 0; i < 4; ++i) {
+                // pairs, since the codes of some Q8_0 blocks are taken from the third on
+                const int e = 32 * b + ((8 * g + 2 * i + (Q8 && NB % 2 == 0 && b % 2 == 0 ? 2 : 0)) & 31);
+                if constexpr (XB) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + base + e);
+                    x[b][2 * i] = bf16_lo(w), x[b][2 * i + 1] = bf16_hi(w);
+                } else {
+                    const float2 w = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + base + e);
+                    x[b][2 * i] = w.x, x[b][2 * i + 1] = w.y;
+                }
+                big = fmaxf(big, fmaxf(fabsf(x[b][2 * i]), fabsf(x[b][2 * i + 1])));
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[b][i]));
         }
         big = fmaxf(big, __shfl_xor(big, 16));
         big = fmaxf(big, __shfl_xor(big, 32));
@@ -87,15 +99,21 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
         const float up = ldexpf(1.0f, 14 - ex);
         qs = ldexpf(1.0f, ex - 14) * a.scale;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+            if ((b & 3) != wave) continue;
+            u4v q[PARTS];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t part[PARTS];
                 split_pair<BF, PARTS>(x[b][2 * i] * up, x[b][2 * i + 1] * up, part);
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) qf[b][k][i] = part[k];
+                for (int k = 0; k < PARTS; ++k) q[k][i] = part[k];
             }
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) s_q[b][k][lane] = q[k];
+        }
     }
+    __syncthreads();
     const float inv_cap = a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
     if (!(a.softcap > 0.f)) qs *= kLog2e;
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
@@ -104,8 +122,8 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
     const int n_pre = (at.pre + 31) >> 5;
     const int w0 = max(n_pre, at.low >> 5), w1 = (at.end + 31) >> 5;
     const int n_tiles = n_pre + max(0, w1 - w0);
-    const int per = (n_tiles + a.splits - 1) / a.splits;
-    const int t0 = (int)blockIdx.z * per, t1 = min(n_tiles, t0 + per);
+    const int per = (n_tiles + w.splits - 1) / w.splits;
+    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
     const int low_last = a.window > 0 ? at.pos + at.tokens - a.window : INT32_MIN;  // every row sees keys from here
 
     const int reach = a.window > 0 ? a.window : INT32_MAX;
@@ -113,14 +131,18 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
     f4v o[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) o[b][0] = o[b][1] = f4v{0.f, 0.f, 0.f, 0.f};
-    float mx = -INFINITY, mref = 0.f, l = 0.f;  // maximum, the same or 0, the lane's part of the sum
+    float mx = -INFINITY, mref = 0.f, l = 0.f;  // maximum, the same less 8 or 0, the lane's part of the sum
     float vlim = 0x1p-30f, vinv = 0x1p30f;      // Q8_0: a power of two that no |d| seen is above, and 1 / it
 
+    // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
+    // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page
     int64_t my_row = -1;
-    int have = 0;
-    for (int t = t0 + wave; t < t1; t += kWaves) {
-        // lane i looks up 16 keys' row in the cache: half i % 2 of the wave's tile i / 2 from here on
-        if (have == 0) {
+    int64_t r0[2];
+    int kb = 0;          // first key of the tile last placed
+    bool whole = false;  // every row sees all of its keys
+    auto place = [&](int t) {
+        const int nth = ((t - t0 - wave) / kWaves) & 31;
+        if (nth == 0) {
             const int tt = t + kWaves * (lane >> 1);
             const int64_t key = 32 * (int64_t)(tt < n_pre ? tt : tt - n_pre + w0) + 16 * (lane & 1);
             my_row = -1;
@@ -130,81 +152,22 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
                 if (pg >= 0 && pg < a.c.n_pages)
                     my_row = ((int64_t)pg * a.c.n_kv + kvh) * a.c.page_size + ((int)key - pidx * a.c.page_size);
             }
-            have = 32;
         }
-        const int from = 2 * (32 - have);
-        --have;
-        int64_t r0[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            r0[u] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, from + u) |
-                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from + u) << 32);
-        const int kb = 32 * (t < n_pre ? t : t - n_pre + w0);
-        const bool paged = r0[0] >= 0 && r0[1] >= 0;
-        const bool whole = paged && ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, at.pos + 1)));
+            r0[u] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, 2 * nth + u) |
+                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
+        kb = 32 * (t < n_pre ? t : t - n_pre + w0);
+        whole = r0[0] >= 0 && r0[1] >= 0 &&
+                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, at.pos + 1)));
+    };
+    // whether any row sees the key in half u of the tile: others may hold anything, and count as 0
+    auto kept = [&](int u, int key) {
+        return (key < at.len) & (r0[u] >= 0) & (((key < at.end) & (key >= at.low)) | (key < at.pre));
+    };
 
-        // ---- loads
-        u4v kf[2][NB];
-        uint32_t vw[2][4][NB], kd[2][4][NB], vd[2][4][NB];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t r = max(r0[u], (int64_t)0);
-            const uint8_t *kbase = a.c.k + r * RB, *vbase = a.c.v + r * RB;
-            const uint8_t* kp = kbase + m * RB;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if constexpr (Q8) {
-                    uint64_t w;
-                    __builtin_memcpy(&w, kp + b * kQ8_0Bytes + 2 + 8 * g, 8);
-                    const uint32_t lo = (uint32_t)w ^ 0x80808080u, hi = (uint32_t)(w >> 32) ^ 0x80808080u;
-                    kf[u][b][0] = codes_f16(lo, 0x04010400u), kf[u][b][1] = codes_f16(lo, 0x04030402u);
-                    kf[u][b][2] = codes_f16(hi, 0x04010400u), kf[u][b][3] = codes_f16(hi, 0x04030402u);
-                } else {
-                    kf[u][b] = *reinterpret_cast<const u4v*>(kp + 64 * b + 16 * g);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* vp = vbase + (4 * g + i) * RB;
-                const uint8_t* kq = kbase + (4 * g + i) * RB;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if constexpr (Q8) {
-                        vw[u][i][b] = ld16(vp + b * kQ8_0Bytes + 2 + 2 * m);
-                        vd[u][i][b] = ld16(vp + b * kQ8_0Bytes);
-                        kd[u][i][b] = ld16(kq + b * kQ8_0Bytes);
-                    } else {
-                        vw[u][i][b] = *reinterpret_cast<const uint32_t*>(vp + 64 * b + 4 * m);
-                    }
-                }
-            }
-        }
-
-        // ---- scores
-        float sc[8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            f4v acc = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (Q8) {
-                f4v sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    acc = f4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = PARTS - 1; k >= 0; --k) acc = mfma16<BF>(kf[u][b], qf[b][k], acc);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(acc[i], h2f(kd[u][i][b]), sum[i]);
-                }
-                acc = sum;
-            } else {
-#pragma unroll
-                for (int k = PARTS - 1; k >= 0; --k)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) acc = mfma16<BF>(kf[u][b], qf[b][k], acc);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[4 * u + i] = acc[i] * qs;
-        }
+    // ---- one tile's scores to P: sc in, p out; raises the running maximum where needed
+    auto soften = [&](float (&sc)[8]) {
         if (a.softcap > 0.f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = a.softcap * kLog2e * tanh_fp32(sc[i] * inv_cap);
@@ -219,20 +182,11 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
             for (int i = 0; i < 8; ++i) {
                 const int u = i >> 2, key = kb + 16 * u + 4 * g + (i & 3);
                 // without branches: this compiler has dropped the assignment where they were nested
-                const bool ok = (key < at.len) & (r0[u] >= 0), pre = key < at.pre;
-                const bool seen = ok & (((key <= p_row) & (p_row - key < reach)) | pre);
-                const bool kept = ok & (((key < at.end) & (key >= at.low)) | pre);
+                const bool seen =
+                    (key < at.len) & (r0[u] >= 0) & (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
                 sc[i] = seen ? sc[i] : -INFINITY;
-                // a key that no row sees may hold anything: 0 times it has to be 0
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if constexpr (Q8) vd[u][i & 3][b] = kept ? vd[u][i & 3][b] : 0;
-                    else vw[u][i & 3][b] = kept ? vw[u][i & 3][b] : 0;
-                }
             }
         }
-
-        // ---- running maximum
         float big = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
         if (__any(big > mx + 7.0f)) {
             big = fmaxf(big, __shfl_xor(big, 16));
@@ -245,22 +199,125 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) o[b][0] *= down, o[b][1] *= down;
         }
-        float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(sc[i] - mref);
-            l += p[i];
+            sc[i] = __builtin_amdgcn_exp2f(sc[i] - mref);
+            l += sc[i];
         }
+    };
 
-        // ---- O^T += V^T P^T
-        if constexpr (Q8) {
+    if constexpr (Q8) {
+        // Staged through LDS, a region of its own for each wave, the keys of a
+        // tile and then its values: the raw blocks (a lane loads 16 consecutive
+        // bytes at a time), and their scales once more, by block and key, so
+        // that a lane finds its four keys' together.  (The scales come from LDS
+        // too: a second load from memory would meet lines still under way.)
+        // The values are loaded while the scores are computed, the next tile's
+        // keys during V^T P^T: registers for one of the two serve both.
+        constexpr int PIECES = 34 * NB;                // 16-byte pieces of 16 keys
+        constexpr int LOADS = (2 * PIECES + 63) / 64;  // of a lane, for 32 keys
+        constexpr int DL = (NB + 1) / 2;               // scales of a lane
+        uint8_t* raw = smem + Q_BYTES + wave * kStage<NB>;
+        uint8_t* tab = raw + 32 * PIECES;
+        u4v in[LOADS];
+        uint32_t din[DL];
+        const int dkey = lane & 31, dblk = lane >> 5;
+        const uint8_t* dsrc = raw + dkey * RB + dblk * kQ8_0Bytes;
+        auto settle = [&]() {  // LDS written by the wave's lanes, read by others of them
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        auto load = [&](const uint8_t* base) {
+            const uint8_t* h0 = base + max(r0[0], (int64_t)0) * RB;
+            const uint8_t* h1 = base + max(r0[1], (int64_t)0) * RB - 16 * PIECES;
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) {
+                const uint32_t i = lane + 64 * j;
+                if (64 * j + 63 < 2 * PIECES || i < 2 * PIECES)
+                    in[j] = *reinterpret_cast<const u4v*>((i < PIECES ? h0 : h1) + 16 * i);
+            }
+        };
+        auto stage = [&]() {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) {
+                const uint32_t i = lane + 64 * j;
+                if (64 * j + 63 < 2 * PIECES || i < 2 * PIECES) *reinterpret_cast<u4v*>(raw + 16 * i) = in[j];
+            }
+            settle();
+#pragma unroll
+            for (int j = 0; j < DL; ++j)
+                if (NB % 2 == 0 || dblk + 2 * j < NB) din[j] = ld16(dsrc + 2 * j * kQ8_0Bytes);
+        };
+        auto scales = [&]() {
+#pragma unroll
+            for (int j = 0; j < DL; ++j)
+                if (NB % 2 == 0 || dblk + 2 * j < NB)
+                    *reinterpret_cast<uint16_t*>(tab + 64 * (dblk + 2 * j) + 2 * dkey) = (uint16_t)din[j];
+            settle();
+        };
+        const uint32_t patch = g == 3 ? 0x07060100u : 0x03020100u;
+        int t = t0 + wave;
+        if (t < t1) {
+            place(t);
+            load(a.c.k);
+        }
+        for (; t < t1; t += kWaves) {
+            stage();
+            load(a.c.v);
+            scales();
+            // ---- scores
+            float sc[8];
+            {
+                f4v sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    u4v qf[PARTS];
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) qf[k] = s_q[b][k][lane];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        // Codes begin 2 bytes behind a multiple of 4 in every
+                        // other block: there lane g takes the 8 from 8g + 2 on
+                        // (as its queries do), and the last lane the block's
+                        // first two for what lies behind its end.  Rows of an
+                        // odd number of blocks shift by themselves.
+                        const uint8_t* blk = raw + (16 * u + m) * RB + b * kQ8_0Bytes;
+                        uint2 w;
+                        if constexpr (NB % 2) {
+                            __builtin_memcpy(&w, blk + 2 + 8 * g, 8);
+                        } else {
+                            const uint32_t* p = reinterpret_cast<const uint32_t*>(blk + (b % 2 ? 2 : 4) + 8 * g);
+                            w.x = p[0], w.y = p[1];
+                            if (b % 2 == 0) w.y = __builtin_amdgcn_perm(*reinterpret_cast<const uint32_t*>(blk), w.y, patch);
+                        }
+                        const u4v kf = codes8_f16(w);
+                        f4v acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = PARTS - 1; k >= 0; --k) acc = mfma16<BF>(kf, qf[k], acc);
+                        const uint2 d = *reinterpret_cast<const uint2*>(tab + 64 * b + 32 * u + 8 * g);
+                        sum[u][0] = fmaf(acc[0], h2f(d.x), sum[u][0]);
+                        sum[u][1] = fmaf(acc[1], h2f(d.x >> 16), sum[u][1]);
+                        sum[u][2] = fmaf(acc[2], h2f(d.y), sum[u][2]);
+                        sum[u][3] = fmaf(acc[3], h2f(d.y >> 16), sum[u][3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sc[i] = sum[i >> 2][i & 3] * qs;
+            }
+            soften(sc);
+            // ---- O^T += V^T (P d)^T
+            settle();
+            stage();
             float dmax = 0.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) dmax = fmaxf(dmax, fabsf(h2f(vd[u][i][b])));
+            for (int j = 0; j < DL; ++j)
+                if (NB % 2 == 0 || dblk + 2 * j < NB) {
+                    if (!whole) din[j] = kept(dkey >> 4, kb + dkey) ? din[j] : 0;
+                    dmax = fmaxf(dmax, fabsf(h2f(din[j])));
+                }
+            scales();
+            place(t + kWaves);  // behind the last tile, row 0 of the cache
+            load(a.c.k);
             if (__any(dmax > vlim)) {
 #pragma unroll
                 for (int k = 1; k < 64; k <<= 1) dmax = fmaxf(dmax, __shfl_xor(dmax, k));
@@ -272,37 +329,93 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
                 for (int b = 0; b < NB; ++b) o[b][0] *= down, o[b][1] *= down;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] *= vinv;
+            for (int i = 0; i < 8; ++i) sc[i] *= vinv;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                u4v pf[PARTS];
+                u4v pf[PARTS], vf[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t part[PARTS];
-                    const int u = i >> 1, k0 = 2 * (i & 1);
-                    split_pair<BF, PARTS>(p[2 * i] * h2f(vd[u][k0][b]), p[2 * i + 1] * h2f(vd[u][k0 + 1][b]), part);
+                for (int u = 0; u < 2; ++u) {
+                    const uint2 d = *reinterpret_cast<const uint2*>(tab + 64 * b + 32 * u + 8 * g);
+                    const uint8_t* v = raw + (16 * u + 4 * g) * RB + b * kQ8_0Bytes + 2 + 2 * m;
 #pragma unroll
-                    for (int k = 0; k < PARTS; ++k) pf[k][i] = part[k];
-                }
-                u4v vf[2];
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t dd = i ? d.y : d.x;
+                        uint32_t part[PARTS];
+                        split_pair<BF, PARTS>(sc[4 * u + 2 * i] * h2f(dd), sc[4 * u + 2 * i + 1] * h2f(dd >> 16), part);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int u = i >> 1, k0 = 2 * (i & 1);
-                    const uint32_t w = (vw[u][k0][b] | vw[u][k0 + 1][b] << 16) ^ 0x80808080u;
-                    vf[0][i] = codes_f16(w, 0x04020400u);
-                    vf[1][i] = codes_f16(w, 0x04030401u);
+                        for (int k = 0; k < PARTS; ++k) pf[k][2 * u + i] = part[k];
+                        const uint32_t w = (ld16(v + 2 * i * RB) | ld16(v + (2 * i + 1) * RB) << 16) ^ 0x80808080u;
+                        vf[0][2 * u + i] = codes_f16(w, 0x04020400u);
+                        vf[1][2 * u + i] = codes_f16(w, 0x04030401u);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int k = PARTS - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
             }
-        } else {
+            settle();
+        }
+    } else {
+        // Rows of 16-bit floats are operands as they lie in memory (K), or after
+        // an exchange of halves between registers (V).  Twelve waves a CU (eight
+        // for wide heads) keep enough loads under way; loading a tile ahead took
+        // the registers of a third of them, and was no faster.
+        u4v kf[2][NB];
+        uint32_t vw[2][4][NB];
+        int64_t b0[2];
+        const uint32_t koff = m * RB + 16 * g, voff = 4 * g * RB + 4 * m;
+        auto load_k = [&]() {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t* kp = a.c.k + b0[u];  // uniform, and 32-bit offsets of the lanes
+#pragma unroll
+                for (int b = 0; b < NB; ++b) kf[u][b] = *reinterpret_cast<const u4v*>(kp + koff + 64 * b);
+            }
+        };
+        auto load_v = [&]() {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* vp = a.c.v + b0[u] + i * RB;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        vw[u][i][b] = *reinterpret_cast<const uint32_t*>(vp + voff + 64 * b);
+                }
+        };
+        for (int t = t0 + wave; t < t1; t += kWaves) {
+            place(t);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) b0[u] = max(r0[u], (int64_t)0) * RB;
+            load_k();
+            load_v();
+            float sc[8];
+            f4v acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int k = PARTS - 1; k >= 0; --k)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const u4v qf = s_q[b][k][lane];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) acc[u] = mfma16<BF>(kf[u][b], qf, acc[u]);
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = acc[i >> 2][i & 3] * qs;
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool keep = kept(i >> 2, kb + 16 * (i >> 2) + 4 * g + (i & 3));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) vw[i >> 2][i & 3][b] = keep ? vw[i >> 2][i & 3][b] : 0;
+                }
+            }
+            soften(sc);
             u4v pf[PARTS];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t part[PARTS];
-                split_pair<BF, PARTS>(p[2 * i], p[2 * i + 1], part);
+                split_pair<BF, PARTS>(sc[2 * i], sc[2 * i + 1], part);
 #pragma unroll
                 for (int k = 0; k < PARTS; ++k) pf[k][i] = part[k];
             }
@@ -311,8 +424,7 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
                 u4v vf[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int u = i >> 1, k0 = 2 * (i & 1);
-                    const uint32_t x = vw[u][k0][b], y = vw[u][k0 + 1][b];
+                    const uint32_t x = vw[i >> 1][2 * (i & 1)][b], y = vw[i >> 1][2 * (i & 1) + 1][b];
                     vf[0][i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
                     vf[1][i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
                 }
@@ -327,7 +439,8 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
     // ---- the four waves' parts: row m, values 8g..8g+7 of each block
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    __shared__ float s_o[kWaves][16][D + 4];
+    __syncthreads();
+    float(*s_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(smem);
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -351,9 +464,11 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
             sum += f * *reinterpret_cast<const f4v*>(&s_o[w][r][e]);
         }
         const int64_t row = (int64_t)(at.row + r / heads) * a.n_q + head0 + r % heads;
-        if (a.splits > 1) {
-            const int64_t part = row * a.splits + blockIdx.z;
-            float* ml = a.work + a.c.n_tokens * a.n_q * a.splits * D;
+        if (a.splits && e == 0 && w.split == 0)
+            join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kSplitRows + r};
+        if (w.splits > 1) {
+            const int64_t part = ((int64_t)item * groups + hb) * kSplitRows + r;
+            float* ml = a.work + a.parts * D;
             if (e == 0) ml[2 * part] = top, ml[2 * part + 1] = den;
             *reinterpret_cast<f4v*>(a.work + part * D + e) = sum;
         } else {
@@ -374,10 +489,10 @@ __global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
 
 template <int CT, int NB, bool XB>
 hipError_t split_typed(const AttnArgs& a, hipStream_t s) {
-    const int64_t items = (a.c.n_tokens >> a.tile_shift) + a.c.n_seqs;
-    const dim3 grid((unsigned)items, (unsigned)(a.c.n_kv * a.chunks), (unsigned)a.splits);
-    hipError_t e = launch(attn_split_kernel<CT, NB, XB>, grid, dim3(256), 0, s, a);
-    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t grid = a.items * a.c.n_kv * a.chunks;
+    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    hipError_t e = launch(attn_split_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    if (e != hipSuccess || !a.splits) return e;
     return launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 

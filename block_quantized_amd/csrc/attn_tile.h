@@ -57,8 +57,7 @@ struct Staged {
 };
 
 template <int CT, int NB, bool XB>
-__global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) void attn_tile_kernel(AttnArgs a,
-                                                                                                    int items) {
+__global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
     constexpr int AP = Q8 && !XB ? 2 : 1;           // parts of K and V
@@ -73,10 +72,10 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     // a long sequence's last tiles see the most keys: they go first.  The
     // heads of a tile are neighbours, so (with 8 of them) each XCD keeps to one
     // head's keys and values.
-    const int groups = a.c.n_kv * a.chunks;
-    TileAt at;
-    if (!find_tile(a, items - 1 - (int)(blockIdx.x / groups), at)) return;
-    const int hb = blockIdx.x % groups;
+    const int groups = a.c.n_kv * a.chunks, item = (int)(blockIdx.x / groups), hb = blockIdx.x % groups;
+    Work w;
+    if (!find_work(a, item, w, true)) return;
+    const TileAt at = w.at;
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = hb / a.chunks, G = a.n_q / a.c.n_kv;
@@ -148,8 +147,8 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     const int n_pre = (at.pre + kKeys - 1) / kKeys;
     const int w0 = max(n_pre, at.low / kKeys), w1 = (at.end + kKeys - 1) / kKeys;
     const int n_tiles = n_pre + max(0, w1 - w0);
-    const int per = (n_tiles + a.splits - 1) / a.splits;
-    const int t0 = (int)blockIdx.z * per, t1 = min(n_tiles, t0 + per);
+    const int per = (n_tiles + w.splits - 1) / w.splits;
+    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
 
     f16v o[NB];
 #pragma unroll
@@ -424,9 +423,11 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     if (32 * wave + r >= rows) return;
     const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
     const float unit = Q8 ? vlim * 0x1p-8f : 1.0f;
-    if (a.splits > 1) {
-        const int64_t part = row * a.splits + blockIdx.z;
-        float* ml = a.work + a.c.n_tokens * a.n_q * a.splits * D;
+    if (a.splits && h == 0 && w.split == 0)
+        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kTileRows + 32 * wave + r};
+    if (w.splits > 1) {
+        const int64_t part = ((int64_t)item * groups + hb) * kTileRows + 32 * wave + r;
+        float* ml = a.work + a.parts * D;
         if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -456,12 +457,10 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
 
 template <int CT, int NB, bool XB>
 hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
-    const int64_t items = (a.c.n_tokens >> a.tile_shift) + a.c.n_seqs;
-    const int64_t groups = items * a.c.n_kv * a.chunks;
-    if (groups >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
-    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)groups, 1, (unsigned)a.splits), dim3(256), 0, s, a,
-                          (int)items);
-    return e != hipSuccess || a.splits == 1 ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
+    const int64_t grid = a.items * a.c.n_kv * a.chunks;
+    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    return e != hipSuccess || !a.splits ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 
 template <int CT, int NB>

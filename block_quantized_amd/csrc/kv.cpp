@@ -94,11 +94,9 @@ int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How qmm_attn divides its work.
 struct Plan {
-    int algo, chunk, chunks, shift, splits;
+    int algo, chunk, chunks, shift, splits, least;
+    int64_t items, parts;
 };
-
-// Tile kernels multiply 128 rows at a time, split kernels 16.
-constexpr int kTileRows = 128, kSplitRows = 16;
 
 int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q) {
     return b->n_tokens * (n_q / c->n_kv) > (int64_t)b->n_seqs * 64 ? 2 : 1;
@@ -111,20 +109,29 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     const int rows = p.algo == 2 ? kTileRows : kSplitRows;
     p.chunk = G < rows ? G : rows;
     p.chunks = (int)up_div(G, p.chunk);
-    while ((2 << p.shift) * p.chunk <= rows) ++p.shift;
-    // split the keys while there are fewer workgroups than two a CU, but leave
-    // each split 256 keys
-    int64_t groups = up_div(b->n_tokens, int64_t(1) << p.shift);
-    const int64_t least = b->n_seqs < b->n_tokens ? b->n_seqs : b->n_tokens;
-    if (groups < least) groups = least;
-    groups *= (int64_t)c->n_kv * p.chunks;
+    // tokens of a row tile: what fits, but no more than a sequence has
+    const int64_t each = up_div(b->n_tokens, b->n_seqs);
+    while ((2 << p.shift) * p.chunk <= rows && (1 << p.shift) < each) ++p.shift;
+    int64_t tiles = (b->n_tokens >> p.shift) + b->n_seqs;  // row tiles at most
+    if (tiles > b->n_tokens) tiles = b->n_tokens;
     int64_t keys = (int64_t)b->table_width * c->page_size;
     if (b->max_kv > 0 && b->max_kv < keys) keys = b->max_kv;
     if (o->window > 0 && !o->prefix && o->window + b->n_tokens < keys) keys = o->window + b->n_tokens;
-    int64_t s = up_div(512, groups);
-    const int64_t most = up_div(keys, 256);
+    // The keys are divided among up to 2048 workgroups, more than run at once, so
+    // that the last of them end together (64 conversations of 8k to 16k keys: 397 us
+    // with 512 workgroups, 362 with 1024, 338 with 2048, 340 with 2560); where that
+    // leaves each below 2048 keys, among fewer, at least 512, two a CU (one of
+    // 131k keys, 8 heads: 76 us with 512, 88 with 2048).  A part keeps 256 keys,
+    // two tiles a wave.  Prompts are split only where their row tiles are fewer than
+    // 512.
+    p.least = 8;
+    const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
+    int64_t s = tiles * keys * heads / 2048;
+    s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
     if (s > most) s = most;
-    p.splits = (int)s;
+    p.splits = keys > 32 * p.least && (p.algo == 1 || s > tiles) ? (int)s : 0;
+    p.items = tiles + p.splits;
+    p.parts = p.splits ? p.items * c->n_kv * p.chunks * rows : 0;
     return p;
 }
 
@@ -147,7 +154,7 @@ int check_attn_sizes(const qmm_kv_cache* c, const qmm_kv_batch* b, int xtype, in
 }
 
 size_t work_bytes_of(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q, const Plan& p) {
-    return p.splits > 1 ? (size_t)b->n_tokens * n_q * p.splits * (c->head_dim + 2) * 4 : 0;
+    return p.splits ? (size_t)p.parts * (c->head_dim + 2) * 4 + (size_t)b->n_tokens * n_q * 16 : 0;
 }
 
 }  // namespace
@@ -251,7 +258,11 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     a.softcap = opts->softcap;
     a.n_q = n_q;
     a.window = opts->window;
+    a.head_dim = cache->head_dim;
     a.splits = p.splits;
+    a.least = p.least;
+    a.items = p.items;
+    a.parts = p.parts;
     a.tile_shift = p.shift;
     a.chunk = p.chunk;
     a.chunks = p.chunks;

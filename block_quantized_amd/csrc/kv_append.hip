@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
     const int step = (int)gridDim.y * 4 * HPW;
 
     for (int64_t t = blockIdx.x; t < a.c.n_tokens; t += gridDim.x) {
-        const int s = find_seq(a.c, (int)t, 0, 0, a.c.n_seqs + 1);
+        const int s = find_seq(a.c, (int)t, a.c.n_seqs + 1);
         if (s < 0 || s >= a.c.n_seqs) continue;  // a row of no sequence
         // index of the token in its sequence, and its cache row (-1: none)
         const int64_t at = (int64_t)a.c.kv_len[s] - clamp_row(a.c.q_start[s + 1], a.c.n_tokens) + t;

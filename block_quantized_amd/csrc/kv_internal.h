@@ -44,26 +44,31 @@ struct AttnArgs {
     const int32_t* prefix;
     int64_t ldq;
     float scale, softcap;
-    int32_t n_q, window, splits;
+    int32_t n_q, window, head_dim;
     int32_t tile_shift;  // log2 of the tokens of a row tile
     int32_t chunk;       // query heads of a row tile
     int32_t chunks;      // row tiles of heads of a key-value head
+    int32_t splits;      // parts that the keys of all row tiles are divided in (more or less); 0: not at all
+    int32_t least;       // blocks of 32 keys that a part has at least
+    int64_t items;       // work items of a head at most
+    int64_t parts;       // rows of the workspace: items x heads x rows of a tile
 };
+
+// Rows of a row tile: of the split and of the tile kernels.
+constexpr int kSplitRows = 16, kTileRows = 128;
 
 #if defined(__HIP_DEVICE_COMPILE__) || defined(__HIPCC__)
 __device__ __forceinline__ int clamp_row(int32_t r, int64_t n) {
     return r < 0 ? 0 : (int64_t)r > n ? (int)n : r;
 }
-// The sequence of work item `item`, the last s with (q_start[s] >> shift) +
-// s * each <= item, by one wavefront: 64 sequences are looked at together.
-// -1 if there is none.
-__device__ __forceinline__ int find_seq(const KvArgs& c, int item, int shift, int each, int count) {
+// The last of the `count` entries of q_start that is at most `row`, by one
+// wavefront: 64 are looked at together.  -1 if there is none.
+__device__ __forceinline__ int find_seq(const KvArgs& c, int row, int count) {
     const int lane = threadIdx.x & 63;
     int n = 0;
     for (int s0 = 0; s0 < count; s0 += 64) {
         const int s = s0 + lane;
-        const bool below = s < count && (clamp_row(c.q_start[s], c.n_tokens) >> shift) + s * each <= item;
-        n += __popcll(__ballot(below));
+        n += __popcll(__ballot(s < count && clamp_row(c.q_start[s], c.n_tokens) <= row));
     }
     return n - 1;
 }
