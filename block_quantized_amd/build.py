@@ -30,8 +30,10 @@ UNITS = {
     "probe.hip": [],
     # stored cache rows are defined to the bit, as the codec's blocks are
     "kv_append.hip": ["-ffp-contract=off"],
-    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-       for kind in ("split", "tile") for cache in ("q8_0", "f16", "bf16")},
+    # scores are no NaN unless the inputs are: no maximum has to quiet one first
+    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-fno-honor-nans"]
+       for kind in ("split", "tile_narrow") for cache in ("q8_0", "f16", "bf16")},
+    **{f"attn_tile_wide_{cache}.hip": ["-fno-honor-nans"] for cache in ("q8_0", "f16", "bf16")},
     "attn_join.hip": [],
     "qmm.cpp": [],
     "kv.cpp": [],

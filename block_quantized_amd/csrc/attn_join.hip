@@ -80,17 +80,18 @@ hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStrea
     }
 }
 
+template <int CT>
+static hipError_t attn_of(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+    if (algo != 2) return launch_attn_split_of<CT>(head_dim, xtype, a, s);
+    return head_dim <= 128 ? launch_attn_tile_narrow<CT>(head_dim, xtype, a, s)
+                           : launch_attn_tile_wide<CT>(head_dim, xtype, a, s);
+}
+
 hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (type) {
-    case QMM_Q8_0:
-        return algo == 2 ? launch_attn_tile_of<QMM_Q8_0>(head_dim, xtype, a, s)
-                         : launch_attn_split_of<QMM_Q8_0>(head_dim, xtype, a, s);
-    case QMM_F16:
-        return algo == 2 ? launch_attn_tile_of<QMM_F16>(head_dim, xtype, a, s)
-                         : launch_attn_split_of<QMM_F16>(head_dim, xtype, a, s);
-    case QMM_BF16:
-        return algo == 2 ? launch_attn_tile_of<QMM_BF16>(head_dim, xtype, a, s)
-                         : launch_attn_split_of<QMM_BF16>(head_dim, xtype, a, s);
+    case QMM_Q8_0: return attn_of<QMM_Q8_0>(algo, head_dim, xtype, a, s);
+    case QMM_F16: return attn_of<QMM_F16>(algo, head_dim, xtype, a, s);
+    case QMM_BF16: return attn_of<QMM_BF16>(algo, head_dim, xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -168,10 +168,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 
     // ---- one tile's scores to P: sc in, p out; raises the running maximum where needed
     auto soften = [&](float (&sc)[8]) {
-        if (a.softcap > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc[i] = a.softcap * kLog2e * tanh_fp32(sc[i] * inv_cap);
-        }
+        if (a.softcap > 0.f) cap_scores(sc, a.softcap, inv_cap);
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -43,7 +43,10 @@ __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
 // 16-byte slot of the keys `oct` (8 in the lanes' order) in the LDS row of
 // value `dim`: an order in which neither the transposing writes (four values
 // apart) nor the operand reads (one apart) meet a bank more often than needed.
-__device__ __forceinline__ int v_slot(int dim, int oct) { return oct ^ (((dim >> 1) ^ (dim >> 4)) & 7); }
+__device__ __forceinline__ int v_slot(int dim, int oct) {
+    const int r = dim & 31;  // the same in each 32 values: reads of them differ by a constant
+    return oct ^ (((r >> 1) ^ (r >> 4)) & 7);
+}
 
 // What a wave has loaded of its 16 keys of a tile.
 template <int CT, int NB>
@@ -64,8 +67,12 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     constexpr int BP = XB ? 1 : BF ? 3 : 2;         // parts of Q and P
     constexpr int KROW = 2 * D + 16;                // bytes of a row of K in LDS
     using St = Staged<CT, NB>;
-    __shared__ __attribute__((aligned(16))) uint8_t s_k[AP][kKeys * KROW];
-    __shared__ __attribute__((aligned(16))) uint8_t s_v[AP][D * kKeys * 2];
+    // Two buffers, and one barrier a tile, where two workgroups a CU still fit.
+    // (Q8_0 needs a barrier between its tile's largest scale and the staging.)
+    constexpr int K_BYTES = kKeys * KROW, V_BYTES = D * kKeys * 2;
+    constexpr int BUFS = !Q8 && 4 * (K_BYTES + V_BYTES) <= 150 * 1024 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) uint8_t s_k[BUFS * AP][K_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t s_v[BUFS * AP][V_BYTES];
     __shared__ float s_big[2][4];  // of a tile, a wave's 16 keys each: the largest |d| (Q8_0),
     __shared__ int s_page[2][4];   // and whether they have a page
 
@@ -111,8 +118,9 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         int ex = 0;
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);
-        const float up = ldexpf(1.0f, 14 - ex);
-        qs = ldexpf(1.0f, ex - 14) * a.scale;
+        // the sign of the scale goes to the queries, and no scale is 0: masked scores stay -inf times it
+        const float up = copysignf(ldexpf(1.0f, 14 - ex), a.scale);
+        qs = fmaxf(ldexpf(1.0f, ex - 14) * fabsf(a.scale), 0x1p-120f);
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b) {
             float x[8];
@@ -179,64 +187,79 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from) << 32);
         const int key0 = kKeys * (t < n_pre ? t : t - n_pre + w0) + 16 * wave;
         paged = row >= 0;
-        const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;
+        const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;  // uniform, with 32-bit offsets of the lanes
         const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
-        // a key that no row sees may hold anything: it counts as 0
-        const bool all = paged & ((key0 + 16 <= at.pre) | ((key0 >= at.low) & (key0 + 16 <= at.end)));
-        auto kept = [&](int key) {
-            return paged & (((key >= at.low) & (key < at.end)) | (key < at.pre));
-        };
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < St::KT; ++i) {
-            const int task = lane + 64 * i;
+            const uint32_t task = lane + 64 * i;
             if constexpr (Q8) {
                 if (NB % 4 == 0 || task < 16 * NB) {
-                    const int key = task / NB, blk = task % NB;
-                    const uint8_t* p = kbase + key * RB + blk * kQ8_0Bytes;
-                    const bool ok = all | kept(key0 + key);
-                    st.k[i][0] = ok ? *reinterpret_cast<const uint16_t*>(p) : 0;
-                    uint64_t w[4];
-                    __builtin_memcpy(w, p + 2, 32);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) st.k[i][1 + 2 * j] = (uint32_t)w[j], st.k[i][2 + 2 * j] = (uint32_t)(w[j] >> 32);
-                    big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+                    const uint8_t* p = kbase + task * kQ8_0Bytes;  // 16 keys' blocks lie one after another
+                    st.k[i][0] = *reinterpret_cast<const uint16_t*>(p);
+                    __builtin_memcpy(&st.k[i][1], p + 2, 32);
                 }
             } else {
-                const int key = task / (4 * NB), c = task % (4 * NB);
-                const u4v w = *reinterpret_cast<const u4v*>(kbase + key * RB + 16 * c);
-                const bool ok = all | kept(key0 + key);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) st.k[i][j] = ok ? w[j] : 0;
+                __builtin_memcpy(st.k[i], reinterpret_cast<const u4v*>(kbase + 16 * task), 16);
             }
         }
 #pragma unroll
         for (int i = 0; i < St::VT; ++i) {
-            const int task = lane + 64 * i;
+            const uint32_t task = lane + 64 * i, oct = task / (8 * NB), c = task % (8 * NB);
             if (NB % 4 == 0 || task < 16 * NB) {
-                const int oct = task / (8 * NB), c = task % (8 * NB);
+                const uint32_t off = 4 * oct * RB + (Q8 ? (c >> 3) * kQ8_0Bytes : 8 * c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int key = 4 * oct + (j & 3) + 2 * (j & 4);  // the lanes' order of 16 keys
-                    const bool ok = all | kept(key0 + key);
+                    const uint8_t* p = vbase + ((j & 3) + 2 * (j & 4)) * RB + off;  // the lanes' order of 16 keys
                     if constexpr (Q8) {
-                        const uint8_t* p = vbase + key * RB + (c >> 3) * kQ8_0Bytes;
-                        st.vd[i][j] = ok ? *reinterpret_cast<const uint16_t*>(p) : 0;
-                        uint32_t w;
-                        __builtin_memcpy(&w, p + 2 + 4 * (c & 7), 4);
-                        st.v[i][j] = w;
-                        big = fmaxf(big, fabsf(h2f(st.vd[i][j])));
+                        st.vd[i][j] = *reinterpret_cast<const uint16_t*>(p);
+                        __builtin_memcpy(&st.v[i][j], p + 2 + 4 * (c & 7), 4);
                     } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(vbase + key * RB + 8 * c);
-                        st.v[i][2 * j] = ok ? w.x : 0, st.v[i][2 * j + 1] = ok ? w.y : 0;
+                        __builtin_memcpy(&st.v[i][2 * j], reinterpret_cast<const uint2*>(p), 8);
                     }
                 }
             }
         }
+        // a key that no row sees may hold anything: it counts as 0
+        if (!(paged & ((key0 + 16 <= at.pre) | ((key0 >= at.low) & (key0 + 16 <= at.end))))) {
+            auto kept = [&](int key) {
+                key += key0;
+                return paged & (((key >= at.low) & (key < at.end)) | (key < at.pre));
+            };
+#pragma unroll
+            for (int i = 0; i < St::KT; ++i) {
+                const bool ok = kept((lane + 64 * i) / (Q8 ? NB : 4 * NB));
+#pragma unroll
+                for (int j = 0; j < (Q8 ? 1 : 4); ++j) st.k[i][j] = ok ? st.k[i][j] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < St::VT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool ok = kept(4 * ((lane + 64 * i) / (8 * NB)) + (j & 3) + 2 * (j & 4));
+                    if constexpr (Q8) {
+                        st.vd[i][j] = ok ? st.vd[i][j] : 0;
+                    } else {
+                        st.v[i][2 * j] = ok ? st.v[i][2 * j] : 0, st.v[i][2 * j + 1] = ok ? st.v[i][2 * j + 1] : 0;
+                    }
+                }
+        }
+        if constexpr (Q8) {
+#pragma unroll
+            for (int i = 0; i < St::KT; ++i)
+                if (NB % 4 == 0 || lane + 64 * i < 16 * NB) big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+#pragma unroll
+            for (int i = 0; i < St::VT; ++i)
+                if (NB % 4 == 0 || lane + 64 * i < 16 * NB)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(h2f(st.vd[i][j])));
+        }
         return big;
     };
-    // Writes what fetch() loaded; Q8_0 values times `inv` (a power of two).
-    auto store = [&](float inv) {
+    // Writes what fetch() loaded to buffer `to`; Q8_0 values times `inv` (a power of two).
+    auto store = [&](float inv, int to) {
+        uint8_t(*s_kt)[K_BYTES] = s_k + AP * to;
+        uint8_t(*s_vt)[V_BYTES] = s_v + AP * to;
 #pragma unroll
         for (int i = 0; i < St::KT; ++i) {
             const int task = lane + 64 * i;
@@ -255,12 +278,12 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                     for (int k = 0; k < AP; ++k)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<u4v*>(&s_k[k][key * KROW + 64 * blk + 16 * j]) =
+                            *reinterpret_cast<u4v*>(&s_kt[k][key * KROW + 64 * blk + 16 * j]) =
                                 u4v{part[4 * j][k], part[4 * j + 1][k], part[4 * j + 2][k], part[4 * j + 3][k]};
                 }
             } else {
                 const int key = 16 * wave + task / (4 * NB), c = task % (4 * NB);
-                *reinterpret_cast<u4v*>(&s_k[0][key * KROW + 16 * c]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
+                *reinterpret_cast<u4v*>(&s_kt[0][key * KROW + 16 * c]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
             }
         }
 #pragma unroll
@@ -285,7 +308,7 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                         }
 #pragma unroll
                         for (int k = 0; k < AP; ++k)
-                            *reinterpret_cast<u4v*>(&s_v[k][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w[k];
+                            *reinterpret_cast<u4v*>(&s_vt[k][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w[k];
                     }
                 } else {
 #pragma unroll
@@ -295,7 +318,7 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                         for (int j = 0; j < 4; ++j)
                             w[j] = __builtin_amdgcn_perm(st.v[i][4 * j + 2 + (e >> 1)], st.v[i][4 * j + (e >> 1)],
                                                          e & 1 ? 0x07060302u : 0x05040100u);
-                        *reinterpret_cast<u4v*>(&s_v[0][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w;
+                        *reinterpret_cast<u4v*>(&s_vt[0][(4 * c + e) * (2 * kKeys) + 16 * v_slot(4 * c + e, oct)]) = w;
                     }
                 }
             }
@@ -313,8 +336,9 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
 
     if (t0 < t1) begin(t0);
     for (int t = t0; t < t1; ++t) {
-        __syncthreads();  // the tile before is multiplied, and s_big of this one told
+        const int buf = BUFS > 1 ? t & 1 : 0;
         float tile_scale = 1.0f;
+        if constexpr (BUFS == 1) __syncthreads();  // the tile before is multiplied, and this one's s_big told
         if constexpr (Q8) {
             const float* b = s_big[t & 1];
             const float big = fminf(fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])), 65504.0f);
@@ -327,95 +351,101 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                 for (int i = 0; i < NB; ++i) o[i] *= down;
             }
             tile_scale = vlim * 0x1p-8f;  // values are staged as d code / tile_scale < 2^15
-            store(0x1p8f / vlim);
+            store(0x1p8f / vlim, buf);
         } else {
-            store(1.0f);
+            store(1.0f, buf);
         }
-        const bool full[2] = {(s_page[t & 1][0] & s_page[t & 1][1]) != 0, (s_page[t & 1][2] & s_page[t & 1][3]) != 0};
-        const bool half[4] = {s_page[t & 1][0] != 0, s_page[t & 1][1] != 0, s_page[t & 1][2] != 0, s_page[t & 1][3] != 0};
         __syncthreads();
+        const bool half[4] = {s_page[t & 1][0] != 0, s_page[t & 1][1] != 0, s_page[t & 1][2] != 0, s_page[t & 1][3] != 0};
+        const uint8_t(*s_kt)[K_BYTES] = s_k + AP * buf;
+        const uint8_t(*s_vt)[V_BYTES] = s_v + AP * buf;
         if (t + 1 < t1) begin(t + 1);
 
         const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
+        // nothing of this tile for any row of the wave
+        if (idle || !((kb < at.pre) || (kb <= p_last && kb < at.len && kb + kKeys - 1 >= low_first))) continue;
+        f16v s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int k0 = kb + 32 * u;
-            // nothing of this half for any row of the wave
-            if (idle || !((k0 < at.pre) || (k0 <= p_last && k0 < at.len && k0 + 31 >= low_first))) continue;
-            f16v s;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = 0.f;
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
 #pragma unroll
             for (int ap = AP - 1; ap >= 0; --ap)
 #pragma unroll
                 for (int b = 0; b < 2 * NB; ++b) {
-                    const u4v kf = *reinterpret_cast<const u4v*>(&s_k[ap][(32 * u + r) * KROW + 32 * b + 16 * h]);
+                    const u4v kf = *reinterpret_cast<const u4v*>(&s_kt[ap][(32 * u + r) * KROW + 32 * b + 16 * h]);
 #pragma unroll
-                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) s = mfma32<BF>(kf, qf[b][k], s);
+                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) s[u] = mfma32<BF>(kf, qf[b][k], s[u]);
                 }
-            const float f = Q8 ? qs * tile_scale : qs;
-            float sc[16];
+        }
+        float f = Q8 ? qs * tile_scale : qs;  // s f: the score, times log2 e without a cap
+        if (capped | (a.slopes != nullptr)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] = s[i] * f;
-            if (capped) {
+            for (int u = 0; u < 2; ++u) {
+                float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[i] = a.softcap * kLog2e * tanh_fp32(sc[i] * inv_cap);
-            }
-            if (a.slopes) {
+                for (int i = 0; i < 16; ++i) x[i] = s[u][i] * f;
+                if (capped) cap_scores(x, a.softcap, inv_cap);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    sc[i] -= slope * fabsf((float)(p_row - (k0 + 8 * (i >> 2) + 4 * h + (i & 3))));
+                    s[u][i] = x[i] - slope * fabsf((float)(p_row - (kb + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3))));
             }
-            const bool whole =
-                full[u] && ((k0 + 32 <= at.pre) || (k0 >= low_last && k0 + 32 <= min(at.len, p_first + 1)));
-            if (!whole) {
+            f = 1.0f;
+        }
+        const bool whole = half[0] && half[1] && half[2] && half[3] &&
+                           ((kb + kKeys <= at.pre) || (kb >= low_last && kb + kKeys <= min(at.len, p_first + 1)));
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+                    const int key = kb + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3);
                     const bool seen = half[2 * u + (i >> 3)] & (key < at.len) &
                                       (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
-                    sc[i] = seen ? sc[i] : -INFINITY;
+                    s[u][i] = seen ? s[u][i] : -INFINITY;
                 }
-            }
-            float big = sc[0];
+        }
+        float big = s[0][0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) big = fmaxf(big, sc[i]);
-            if (__any(big > mx + 7.0f)) {
-                big = fmaxf(big, __shfl_xor(big, 32));
-                const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
-                const float down = __builtin_amdgcn_exp2f(mx - ref);
-                mx = top;
-                mref = ref - 8.0f;
-                l *= down;
+        for (int i = 1; i < 32; ++i) big = fmaxf(big, s[i >> 4][i & 15]);
+        if (__any(big * f > mx + 7.0f)) {
+            big = fmaxf(big, __shfl_xor(big, 32)) * f;
+            const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
+            const float down = __builtin_amdgcn_exp2f(mx - ref);
+            mx = top;
+            mref = ref - 8.0f;
+            l *= down;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) o[b] *= down;
-            }
+            for (int b = 0; b < NB; ++b) o[b] *= down;
+        }
+        // P of the second half between the products of the first
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sc[i] = __builtin_amdgcn_exp2f(sc[i] - mref);
-                l += sc[i];
-            }
+        for (int u = 0; u < 2; ++u) {
+            u4v pf[2][BP];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                u4v pf[BP];
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(s[u][8 * kk + 2 * i], f, -mref));
+                    const float y = __builtin_amdgcn_exp2f(fmaf(s[u][8 * kk + 2 * i + 1], f, -mref));
+                    l += x + y;
                     uint32_t part[BP];
-                    split_pair<BF, BP>(sc[8 * kk + 2 * i], sc[8 * kk + 2 * i + 1], part);
+                    split_pair<BF, BP>(x, y, part);
 #pragma unroll
-                    for (int k = 0; k < BP; ++k) pf[k][i] = part[k];
+                    for (int k = 0; k < BP; ++k) pf[kk][k][i] = part[k];
                 }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int ap = AP - 1; ap >= 0; --ap) {
                         const int dim = 32 * b + r;
                         const u4v vf = *reinterpret_cast<const u4v*>(
-                            &s_v[ap][dim * (2 * kKeys) + 16 * v_slot(dim, 4 * u + 2 * kk + h)]);
+                            &s_vt[ap][dim * (2 * kKeys) + 16 * v_slot(dim, 4 * u + 2 * kk + h)]);
 #pragma unroll
-                        for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[b] = mfma32<BF>(vf, pf[k], o[b]);
+                        for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[b] = mfma32<BF>(vf, pf[kk][k], o[b]);
                     }
-            }
         }
     }
 
@@ -470,12 +500,21 @@ hipError_t tile_x(int xtype, const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// Heads of up to 128 values, and wider ones: units of their own, since the
+// first keep accumulators in vector registers and the second need both files.
 template <int CT>
-hipError_t launch_attn_tile_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
     case 64: return tile_x<CT, 2>(xtype, a, s);
     case 96: return tile_x<CT, 3>(xtype, a, s);
     case 128: return tile_x<CT, 4>(xtype, a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+template <int CT>
+hipError_t launch_attn_tile_wide(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+    switch (head_dim) {
     case 192: return tile_x<CT, 6>(xtype, a, s);
     case 256: return tile_x<CT, 8>(xtype, a, s);
     default: return hipErrorInvalidValue;

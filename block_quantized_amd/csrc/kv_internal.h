@@ -82,7 +82,9 @@ hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnAr
 template <int CT>
 hipError_t launch_attn_split_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 template <int CT>
-hipError_t launch_attn_tile_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+template <int CT>
+hipError_t launch_attn_tile_wide(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 
 }  // namespace qmm
