@@ -32,8 +32,7 @@ UNITS = {
     "kv_append.hip": ["-ffp-contract=off"],
     # scores are no NaN unless the inputs are: no maximum has to quiet one first
     **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-fno-honor-nans"]
-       for kind in ("split", "tile_narrow") for cache in ("q8_0", "f16", "bf16")},
-    **{f"attn_tile_wide_{cache}.hip": ["-fno-honor-nans"] for cache in ("q8_0", "f16", "bf16")},
+       for kind in ("split", "tile_narrow", "tile_wide") for cache in ("q8_0", "f16", "bf16")},
     "attn_join.hip": [],
     "qmm.cpp": [],
     "kv.cpp": [],

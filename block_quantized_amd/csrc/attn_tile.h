@@ -1,19 +1,22 @@
 // attn_tile.h — attention over a paged cache for many query rows a
 // sequence: a workgroup takes 128 query rows (tokens x the query heads of one
-// key-value head) and walks the keys in tiles of 64, which its four waves
-// stage in LDS together and each multiplies with 32 rows.
+// key-value head) and walks the keys in tiles of 64, which its waves stage in
+// LDS together and each multiplies with its 32 (or 16) rows.
 //
-// With 32x32x16 MFMAs, as in the split kernels:
+// With 32x32x16 MFMAs (16x16x32 in parentheses), as in the split kernels:
 //   S^T = K Q^T      lane (r, h) = (lane % 32, lane / 32) gets the scores of
-//                    row r with the keys 8 i + 4 h .. + 3 of a 32-key half;
-//   O^T += V^T P^T   the keys of a 16-key step in the order the lanes hold
-//                    their scores in, so P never leaves its lane.
+//                    row r with 4 keys of each 8 of the tile (of each 16);
+//   O^T += V^T P^T   the keys of a step in the order the lanes hold their
+//                    scores in, so P never leaves its lane.
 // K lies in LDS as it is (rows 16 bytes apart from a multiple of the banks),
 // V transposed, a row of 64 keys a value, in that key order: both are read as
-// the MFMAs' A operands with 16-byte loads that meet no bank twice.
+// the MFMAs' A operands with 16-byte loads.  The larger MFMAs read half as
+// much of LDS for a product; the smaller ones need half the registers a wave,
+// which wide heads and three-part queries take (with eight waves of 16 rows,
+// two a SIMD, instead of four of 32 and one).
 //
-// A wave stages the 16 keys of its number in each tile, so where they lie in
-// the cache is one page lookup, the same for its lanes.  The next tile's
+// A wave stages the 16 (8) keys of its number in each tile, so where they lie
+// in the cache is one page lookup, the same for its lanes.  The next tile's
 // loads are issued before a tile is multiplied.
 //
 // Exactness: bf16 queries take one product with 16-bit P.  fp32 queries and P
@@ -31,13 +34,17 @@ namespace {
 constexpr int kKeys = 64;  // keys of a tile
 
 template <bool BF>
-__device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
+__device__ __forceinline__ f16v mfma_of(u4v a, u4v b, f16v c) {
     if constexpr (BF)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), c, 0,
                                                        0, 0);
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), c,
                                                       0, 0, 0);
+}
+template <bool BF>
+__device__ __forceinline__ f4v mfma_of(u4v a, u4v b, f4v c) {
+    return mfma16<BF>(a, b, c);
 }
 
 // 16-byte slot of the keys `oct` (8 in the lanes' order) in the LDS row of
@@ -48,33 +55,43 @@ __device__ __forceinline__ int v_slot(int dim, int oct) {
     return oct ^ (((r >> 1) ^ (r >> 4)) & 7);
 }
 
-// What a wave has loaded of its 16 keys of a tile.
-template <int CT, int NB>
+// What a wave has loaded of its KEYS keys of a tile.
+template <int CT, int NB, int KEYS>
 struct Staged {
     static constexpr bool Q8 = CT == QMM_Q8_0;
-    static constexpr int KT = Q8 ? (NB + 3) / 4 : NB;  // tasks of a lane: a block, or 16 bytes
-    static constexpr int VT = (NB + 3) / 4;            // tasks of a lane: 8 keys x 4 values
+    static constexpr int KT = ((Q8 ? 1 : 4) * KEYS * NB + 63) / 64;  // tasks of a lane: a block, or 16 bytes
+    static constexpr int VT = (KEYS * NB + 63) / 64;                        // tasks of a lane: 8 keys x 4 values
     uint32_t k[KT][Q8 ? 9 : 4];
     uint32_t v[VT][Q8 ? 8 : 16];
     uint32_t vd[VT][Q8 ? 8 : 1];
 };
 
+// Parts of Q and P, and rows of a wave.
+// The largest group of operands, up to `most`, that n of them divide into.
+constexpr int group_of(int n, int most) { return n % most ? group_of(n, most - 1) : most; }
+constexpr int q_parts(int ct, bool xb) { return xb ? 1 : ct == QMM_BF16 ? 3 : 2; }
+constexpr int wave_rows(int ct, int nb, bool xb) { return nb > 4 || q_parts(ct, xb) == 3 ? 16 : 32; }
+
 template <int CT, int NB, bool XB>
-__global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void attn_tile_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
-    constexpr int AP = Q8 && !XB ? 2 : 1;           // parts of K and V
-    constexpr int BP = XB ? 1 : BF ? 3 : 2;         // parts of Q and P
-    constexpr int KROW = 2 * D + 16;                // bytes of a row of K in LDS
-    using St = Staged<CT, NB>;
-    // Two buffers, and one barrier a tile, where two workgroups a CU still fit.
+    constexpr int AP = Q8 && !XB ? 2 : 1, BP = q_parts(CT, XB);  // parts of K and V, of Q and P
+    constexpr int R = wave_rows(CT, NB, XB), W = kTileRows / R;  // rows of a wave, waves
+    constexpr int GROUPS = 64 / R, KS = 8 * GROUPS;              // lanes of a row, values (or keys) of an MFMA's step
+    constexpr int KPW = kKeys / W;                               // keys that a wave stages
+    constexpr int VL = R * R / 64, NO = D / R;                   // values of an accumulator, accumulators
+    typedef float accv __attribute__((ext_vector_type(VL)));
+    constexpr int KROW = 2 * D + 16;                             // bytes of a row of K in LDS
+    using St = Staged<CT, NB, KPW>;
+    // Two buffers, and one barrier a tile, where eight waves a CU still fit.
     // (Q8_0 needs a barrier between its tile's largest scale and the staging.)
     constexpr int K_BYTES = kKeys * KROW, V_BYTES = D * kKeys * 2;
-    constexpr int BUFS = !Q8 && 4 * (K_BYTES + V_BYTES) <= 150 * 1024 ? 2 : 1;
+    constexpr int BUFS = !Q8 && 2 * (K_BYTES + V_BYTES) * (8 / W) <= 150 * 1024 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) uint8_t s_k[BUFS * AP][K_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t s_v[BUFS * AP][V_BYTES];
-    __shared__ float s_big[2][4];  // of a tile, a wave's 16 keys each: the largest |d| (Q8_0),
-    __shared__ int s_page[2][4];   // and whether they have a page
+    __shared__ float s_big[2][W];  // of a tile, a wave's keys each: the largest |d| (Q8_0),
+    __shared__ int s_page[2][W];   // and whether they have a page
 
     // a long sequence's last tiles see the most keys: they go first.  The
     // heads of a tile are neighbours, so (with 8 of them) each XCD keeps to one
@@ -83,37 +100,47 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     Work w;
     if (!find_work(a, item, w, true)) return;
     const TileAt at = w.at;
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int lane = threadIdx.x & 63, r = lane % R, h = lane / R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = hb / a.chunks, G = a.n_q / a.c.n_kv;
     const int head0 = kvh * G + (hb % a.chunks) * a.chunk;
     const int heads = min(a.chunk, kvh * G + G - head0);
     const int rows = at.tokens * heads;
-    const int mr = min(32 * wave + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
+    const int mr = min(R * wave + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
     const int p_row = at.pos + mt;
     // the positions of the wave's first and last row
-    const int p_first = at.pos + min(32 * wave, rows - 1) / heads, p_last = at.pos + min(32 * wave + 31, rows - 1) / heads;
-    const bool idle = 32 * wave >= rows;
+    const int p_first = at.pos + min(R * wave, rows - 1) / heads, p_last = at.pos + min(R * wave + R - 1, rows - 1) / heads;
+    const bool idle = R * wave >= rows;
+    // the key, in its tile, of value i of the lane's scores
+    auto key_of = [&](int i) {
+        return R == 32 ? 32 * (i >> 4) + 8 * ((i & 15) >> 2) + 4 * h + (i & 3)
+                       : 32 * (i >> 3) + 8 * h + 4 * ((i >> 2) & 1) + (i & 3);
+    };
+    // LDS offset of 16 bytes of K, columns col .. of 8 values.  (With 16 rows a wave the lanes of an operand
+    // read the keys 0..3 of each 8: those of the upper half turn to other columns to miss the lower ones' banks,
+    // where a row is whole eights of columns.)
+    auto k_at = [&](int key, int col) { return key * KROW + 16 * (R == 32 || NB % 2 ? col : col ^ ((key >> 2) & 4)); };
 
-    // ---- the queries, as B operands: lane (r, h) holds the values 8h..8h+7 of each 16
-    u4v qf[2 * NB][BP];
+    // ---- the queries, as B operands: lane (r, h) holds the values 8h..8h+7 of each step
+    u4v qf[D / KS][BP];
     float qs;
     {
         const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D + 8 * h;
         float big = 0.f;
         // twice over the row: the first for its largest value (the second comes from L1)
 #pragma unroll
-        for (int b = 0; b < 2 * NB; ++b) {
+        for (int b = 0; b < D / KS; ++b) {
             if constexpr (XB) {
-                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + 16 * b);
+                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + KS * b);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
             } else {
-                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + 16 * b);
+                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + KS * b);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(p[0][i]), fabsf(p[1][i])));
             }
         }
+        if constexpr (R == 16) big = fmaxf(big, __shfl_xor(big, 16));
         big = fmaxf(big, __shfl_xor(big, 32));
         int ex = 0;
         frexpf(big, &ex);
@@ -122,14 +149,14 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         const float up = copysignf(ldexpf(1.0f, 14 - ex), a.scale);
         qs = fmaxf(ldexpf(1.0f, ex - 14) * fabsf(a.scale), 0x1p-120f);
 #pragma unroll
-        for (int b = 0; b < 2 * NB; ++b) {
+        for (int b = 0; b < D / KS; ++b) {
             float x[8];
             if constexpr (XB) {
-                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + 16 * b);
+                const u4v w = *reinterpret_cast<const u4v*>(static_cast<const uint16_t*>(a.q) + base + KS * b);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
             } else {
-                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + 16 * b);
+                const f4v* p = reinterpret_cast<const f4v*>(static_cast<const float*>(a.q) + base + KS * b);
                 const f4v u = p[0], w = p[1];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = u[i], x[4 + i] = w[i];
@@ -158,23 +185,25 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
     const int per = (n_tiles + w.splits - 1) / w.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
 
-    f16v o[NB];
+    accv o[NO];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int c = 0; c < NO; ++c)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+        for (int i = 0; i < VL; ++i) o[c][i] = 0.f;
     float mx = -INFINITY, mref = 0.f, l = 0.f;
     float vlim = 0x1p-30f;  // Q8_0: a power of two that no |d| so far is above
 
-    int64_t my_row = -1;  // lane i: where the wave's 16 keys of tile i from here on begin in the cache, or -1
+    int64_t my_row = -1;  // lane i: where the wave's keys of tile i from here on begin in the cache, or -1
     St st;
     bool paged = false;
+    // key j of the first of the wave's runs of 8 keys in the lanes' order (the second run begins 4 behind it)
+    auto nth = [](int j) { return R == 32 ? (j & 3) + 2 * (j & 4) : j; };
     // Loads the wave's keys of tile t; `big`: the largest |d| of the tile's Q8_0 blocks that this wave holds.
     auto fetch = [&](int t) -> float {
         const int from = (t - t0) & 63;
         if (from == 0) {
             const int tt = t + lane;
-            const int64_t key = (int64_t)kKeys * (tt < n_pre ? tt : tt - n_pre + w0) + 16 * wave;
+            const int64_t key = (int64_t)kKeys * (tt < n_pre ? tt : tt - n_pre + w0) + KPW * wave;
             my_row = -1;
             if (tt < t1 && key < at.len) {
                 const int pidx = (int)key / a.c.page_size;
@@ -185,7 +214,7 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         }
         const int64_t row = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, from) |
                                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from) << 32);
-        const int key0 = kKeys * (t < n_pre ? t : t - n_pre + w0) + 16 * wave;
+        const int key0 = kKeys * (t < n_pre ? t : t - n_pre + w0) + KPW * wave;
         paged = row >= 0;
         const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;  // uniform, with 32-bit offsets of the lanes
         const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
@@ -194,23 +223,23 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         for (int i = 0; i < St::KT; ++i) {
             const uint32_t task = lane + 64 * i;
             if constexpr (Q8) {
-                if (NB % 4 == 0 || task < 16 * NB) {
-                    const uint8_t* p = kbase + task * kQ8_0Bytes;  // 16 keys' blocks lie one after another
+                if (KPW * NB % 64 == 0 || task < KPW * NB) {
+                    const uint8_t* p = kbase + task * kQ8_0Bytes;  // the keys' blocks lie one after another
                     st.k[i][0] = *reinterpret_cast<const uint16_t*>(p);
                     __builtin_memcpy(&st.k[i][1], p + 2, 32);
                 }
-            } else {
+            } else if (KPW * NB % 16 == 0 || task < 4 * KPW * NB) {
                 __builtin_memcpy(st.k[i], reinterpret_cast<const u4v*>(kbase + 16 * task), 16);
             }
         }
 #pragma unroll
         for (int i = 0; i < St::VT; ++i) {
             const uint32_t task = lane + 64 * i, oct = task / (8 * NB), c = task % (8 * NB);
-            if (NB % 4 == 0 || task < 16 * NB) {
+            if (KPW * NB % 64 == 0 || task < KPW * NB) {
                 const uint32_t off = 4 * oct * RB + (Q8 ? (c >> 3) * kQ8_0Bytes : 8 * c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint8_t* p = vbase + ((j & 3) + 2 * (j & 4)) * RB + off;  // the lanes' order of 16 keys
+                    const uint8_t* p = vbase + nth(j) * RB + off;
                     if constexpr (Q8) {
                         st.vd[i][j] = *reinterpret_cast<const uint16_t*>(p);
                         __builtin_memcpy(&st.v[i][j], p + 2 + 4 * (c & 7), 4);
@@ -221,7 +250,7 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
             }
         }
         // a key that no row sees may hold anything: it counts as 0
-        if (!(paged & ((key0 + 16 <= at.pre) | ((key0 >= at.low) & (key0 + 16 <= at.end))))) {
+        if (!(paged & ((key0 + KPW <= at.pre) | ((key0 >= at.low) & (key0 + KPW <= at.end))))) {
             auto kept = [&](int key) {
                 key += key0;
                 return paged & (((key >= at.low) & (key < at.end)) | (key < at.pre));
@@ -236,7 +265,7 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
             for (int i = 0; i < St::VT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const bool ok = kept(4 * ((lane + 64 * i) / (8 * NB)) + (j & 3) + 2 * (j & 4));
+                    const bool ok = kept(4 * ((lane + 64 * i) / (8 * NB)) + nth(j));
                     if constexpr (Q8) {
                         st.vd[i][j] = ok ? st.vd[i][j] : 0;
                     } else {
@@ -247,10 +276,10 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         if constexpr (Q8) {
 #pragma unroll
             for (int i = 0; i < St::KT; ++i)
-                if (NB % 4 == 0 || lane + 64 * i < 16 * NB) big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB) big = fmaxf(big, fabsf(h2f(st.k[i][0])));
 #pragma unroll
             for (int i = 0; i < St::VT; ++i)
-                if (NB % 4 == 0 || lane + 64 * i < 16 * NB)
+                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(h2f(st.vd[i][j])));
         }
@@ -264,8 +293,8 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         for (int i = 0; i < St::KT; ++i) {
             const int task = lane + 64 * i;
             if constexpr (Q8) {
-                if (NB % 4 == 0 || task < 16 * NB) {
-                    const int key = 16 * wave + task / NB, blk = task % NB;
+                if (KPW * NB % 64 == 0 || task < KPW * NB) {
+                    const int key = KPW * wave + task / NB, blk = task % NB;
                     const float d = h2f(st.k[i][0]) * inv;
                     uint32_t part[16][AP];
 #pragma unroll
@@ -278,19 +307,19 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
                     for (int k = 0; k < AP; ++k)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<u4v*>(&s_kt[k][key * KROW + 64 * blk + 16 * j]) =
+                            *reinterpret_cast<u4v*>(&s_kt[k][k_at(key, 4 * blk + j)]) =
                                 u4v{part[4 * j][k], part[4 * j + 1][k], part[4 * j + 2][k], part[4 * j + 3][k]};
                 }
-            } else {
-                const int key = 16 * wave + task / (4 * NB), c = task % (4 * NB);
-                *reinterpret_cast<u4v*>(&s_kt[0][key * KROW + 16 * c]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
+            } else if (KPW * NB % 16 == 0 || task < 4 * KPW * NB) {
+                const int key = KPW * wave + task / (4 * NB), c = task % (4 * NB);
+                *reinterpret_cast<u4v*>(&s_kt[0][k_at(key, c)]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
             }
         }
 #pragma unroll
         for (int i = 0; i < St::VT; ++i) {
             const int task = lane + 64 * i;
-            if (NB % 4 == 0 || task < 16 * NB) {
-                const int oct = 2 * wave + task / (8 * NB), c = task % (8 * NB);
+            if (KPW * NB % 64 == 0 || task < KPW * NB) {
+                const int oct = KPW / 8 * wave + task / (8 * NB), c = task % (8 * NB);
                 if constexpr (Q8) {
                     float d[8];
 #pragma unroll
@@ -340,15 +369,17 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         float tile_scale = 1.0f;
         if constexpr (BUFS == 1) __syncthreads();  // the tile before is multiplied, and this one's s_big told
         if constexpr (Q8) {
-            const float* b = s_big[t & 1];
-            const float big = fminf(fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])), 65504.0f);
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i]);
+            big = fminf(big, 65504.0f);
             if (big > vlim) {  // the same in every wave
                 int ex;
                 frexpf(big, &ex);
                 const float lim = ldexpf(1.0f, ex), down = vlim / lim;
                 vlim = lim;
 #pragma unroll
-                for (int i = 0; i < NB; ++i) o[i] *= down;
+                for (int c = 0; c < NO; ++c) o[c] *= down;
             }
             tile_scale = vlim * 0x1p-8f;  // values are staged as d code / tile_scale < 2^15
             store(0x1p8f / vlim, buf);
@@ -356,7 +387,9 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
             store(1.0f, buf);
         }
         __syncthreads();
-        const bool half[4] = {s_page[t & 1][0] != 0, s_page[t & 1][1] != 0, s_page[t & 1][2] != 0, s_page[t & 1][3] != 0};
+        bool page[4];  // of each 16 keys
+#pragma unroll
+        for (int i = 0; i < 4; ++i) page[i] = s_page[t & 1][W / 4 * i] != 0;
         const uint8_t(*s_kt)[K_BYTES] = s_k + AP * buf;
         const uint8_t(*s_vt)[V_BYTES] = s_v + AP * buf;
         if (t + 1 < t1) begin(t + 1);
@@ -364,51 +397,78 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
         const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
         // nothing of this tile for any row of the wave
         if (idle || !((kb < at.pre) || (kb <= p_last && kb < at.len && kb + kKeys - 1 >= low_first))) continue;
-        f16v s[2];
+        // Operands come from LDS some at a time, the next ones while these are
+        // multiplied: left to itself the compiler waits for each before its use.
+        constexpr int STEPS = D / KS, SUBS = kKeys / R;  // of an accumulator's products, accumulators of scores
+        constexpr int GK = group_of(SUBS * AP * STEPS, BP > 1 ? 2 : 4), GV = group_of(NO * AP, BP > 1 ? 2 : 4);
+        float s[R];
+        {
+            accv acc[SUBS];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+                for (int i = 0; i < VL; ++i) acc[u][i] = 0.f;
+            constexpr int N = SUBS * AP * STEPS;  // (keys, part, values)
+            auto operand = [&](int i) {
+                const int u = i / (STEPS * AP), ap = AP - 1 - i / STEPS % AP, b = i % STEPS;
+                const int key = R == 32 ? 32 * u + r : 32 * (u >> 1) + 8 * (r >> 2) + 4 * (u & 1) + (r & 3);
+                return *reinterpret_cast<const u4v*>(&s_kt[ap][k_at(key, GROUPS * b + h)]);
+            };
+            u4v kf[2][GK];
 #pragma unroll
-            for (int ap = AP - 1; ap >= 0; --ap)
+            for (int j = 0; j < GK; ++j) kf[0][j] = operand(j);
 #pragma unroll
-                for (int b = 0; b < 2 * NB; ++b) {
-                    const u4v kf = *reinterpret_cast<const u4v*>(&s_kt[ap][(32 * u + r) * KROW + 32 * b + 16 * h]);
+            for (int i = 0; i < N; i += GK) {
+                if (i + GK < N) {
 #pragma unroll
-                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) s[u] = mfma32<BF>(kf, qf[b][k], s[u]);
+                    for (int j = 0; j < GK; ++j) kf[(i / GK + 1) & 1][j] = operand(i + GK + j);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < GK; ++j) {
+                    const int u = (i + j) / (STEPS * AP), ap = AP - 1 - (i + j) / STEPS % AP, b = (i + j) % STEPS;
+#pragma unroll
+                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) acc[u] = mfma_of<BF>(kf[(i / GK) & 1][j], qf[b][k], acc[u]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) s[i] = acc[i / VL][i % VL];
         }
+        auto v_operand = [&](int i) {  // (step, values, part)
+            const int kk = i / (NO * AP), c = i / AP % NO, ap = AP - 1 - i % AP, dim = R * c + r;
+            return *reinterpret_cast<const u4v*>(&s_vt[ap][dim * (2 * kKeys) + 16 * v_slot(dim, GROUPS * kk + h)]);
+        };
+        u4v vf[2][GV];
+#pragma unroll
+        for (int j = 0; j < GV; ++j) vf[0][j] = v_operand(j);
+        __builtin_amdgcn_sched_barrier(0);
         float f = Q8 ? qs * tile_scale : qs;  // s f: the score, times log2 e without a cap
         if (capped | (a.slopes != nullptr)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x[16];
+            for (int i = 0; i < R; ++i) s[i] *= f;
+            if (capped) cap_scores(s, a.softcap, inv_cap);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = s[u][i] * f;
-                if (capped) cap_scores(x, a.softcap, inv_cap);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[u][i] = x[i] - slope * fabsf((float)(p_row - (kb + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3))));
-            }
+            for (int i = 0; i < R; ++i) s[i] -= slope * fabsf((float)(p_row - (kb + key_of(i))));
             f = 1.0f;
         }
-        const bool whole = half[0] && half[1] && half[2] && half[3] &&
+        const bool whole = page[0] && page[1] && page[2] && page[3] &&
                            ((kb + kKeys <= at.pre) || (kb >= low_last && kb + kKeys <= min(at.len, p_first + 1)));
         if (!whole) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = kb + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3);
-                    const bool seen = half[2 * u + (i >> 3)] & (key < at.len) &
-                                      (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
-                    s[u][i] = seen ? s[u][i] : -INFINITY;
-                }
+            for (int i = 0; i < R; ++i) {
+                const int key = kb + key_of(i);
+                const bool paged = R == 32 ? page[i >> 3] : (h >> 1 ? page[2 * (i >> 3) + 1] : page[2 * (i >> 3)]);
+                const bool seen =
+                    paged & (key < at.len) & (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
+                s[i] = seen ? s[i] : -INFINITY;
+            }
         }
-        float big = s[0][0];
+        float big = s[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) big = fmaxf(big, s[i >> 4][i & 15]);
+        for (int i = 1; i < R; ++i) big = fmaxf(big, s[i]);
         if (__any(big * f > mx + 7.0f)) {
+            if constexpr (R == 16) big = fmaxf(big, __shfl_xor(big, 16));
             big = fmaxf(big, __shfl_xor(big, 32)) * f;
             const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
             const float down = __builtin_amdgcn_exp2f(mx - ref);
@@ -416,64 +476,67 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
             mref = ref - 8.0f;
             l *= down;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) o[b] *= down;
+            for (int c = 0; c < NO; ++c) o[c] *= down;
         }
-        // P of the second half between the products of the first
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            u4v pf[2][BP];
+        for (int kk = 0; kk < kKeys / KS; ++kk) {
+            u4v pf[BP];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+            for (int i = 0; i < 4; ++i) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[8 * kk + 2 * i], f, -mref));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[8 * kk + 2 * i + 1], f, -mref));
+                l += x + y;
+                uint32_t part[BP];
+                split_pair<BF, BP>(x, y, part);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(s[u][8 * kk + 2 * i], f, -mref));
-                    const float y = __builtin_amdgcn_exp2f(fmaf(s[u][8 * kk + 2 * i + 1], f, -mref));
-                    l += x + y;
-                    uint32_t part[BP];
-                    split_pair<BF, BP>(x, y, part);
+                for (int k = 0; k < BP; ++k) pf[k][i] = part[k];
+            }
+            constexpr int N = NO * AP;
 #pragma unroll
-                    for (int k = 0; k < BP; ++k) pf[kk][k][i] = part[k];
+            for (int i = kk * N; i < kk * N + N; i += GV) {
+                if (i + GV < kKeys / KS * N) {
+#pragma unroll
+                    for (int j = 0; j < GV; ++j) vf[(i / GV + 1) & 1][j] = v_operand(i + GV + j);
                 }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+                for (int j = 0; j < GV; ++j) {
+                    const int c = (i + j) / AP % NO, ap = AP - 1 - (i + j) % AP;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int ap = AP - 1; ap >= 0; --ap) {
-                        const int dim = 32 * b + r;
-                        const u4v vf = *reinterpret_cast<const u4v*>(
-                            &s_vt[ap][dim * (2 * kKeys) + 16 * v_slot(dim, 4 * u + 2 * kk + h)]);
-#pragma unroll
-                        for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[b] = mfma32<BF>(vf, pf[kk][k], o[b]);
-                    }
+                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[c] = mfma_of<BF>(vf[(i / GV) & 1][j], pf[k], o[c]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
 
+    if constexpr (R == 16) l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (32 * wave + r >= rows) return;
+    if (R * wave + r >= rows) return;
     const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
     const float unit = Q8 ? vlim * 0x1p-8f : 1.0f;
     if (a.splits && h == 0 && w.split == 0)
-        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kTileRows + 32 * wave + r};
+        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kTileRows + R * wave + r};
+    // accumulator c, value i: value R c + 8 (i / 4) + 4 h + i % 4 of the row
     if (w.splits > 1) {
-        const int64_t part = ((int64_t)item * groups + hb) * kTileRows + 32 * wave + r;
+        const int64_t part = ((int64_t)item * groups + hb) * kTileRows + R * wave + r;
         float* ml = a.work + a.parts * D;
         if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int c = 0; c < NO; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f4v*>(a.work + part * D + 32 * b + 8 * i + 4 * h) =
-                    f4v{o[b][4 * i] * unit, o[b][4 * i + 1] * unit, o[b][4 * i + 2] * unit, o[b][4 * i + 3] * unit};
+            for (int i = 0; i < VL; i += 4)
+                *reinterpret_cast<f4v*>(a.work + part * D + R * c + 2 * i + 4 * h) =
+                    f4v{o[c][i] * unit, o[c][i + 1] * unit, o[c][i + 2] * unit, o[c][i + 3] * unit};
         return;
     }
     const float inv = (l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l) * unit;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int c = 0; c < NO; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x0 = o[b][4 * i] * inv, x1 = o[b][4 * i + 1] * inv, x2 = o[b][4 * i + 2] * inv, x3 = o[b][4 * i + 3] * inv;
-            const int64_t e = row * D + 32 * b + 8 * i + 4 * h;
+        for (int i = 0; i < VL; i += 4) {
+            const float x0 = o[c][i] * inv, x1 = o[c][i + 1] * inv, x2 = o[c][i + 2] * inv, x3 = o[c][i + 3] * inv;
+            const int64_t e = row * D + R * c + 2 * i + 4 * h;
             if constexpr (XB) {
                 uint32_t w0[1], w1[1];
                 split_pair<true, 1>(x0, x1, w0);
@@ -488,8 +551,9 @@ __global__ __launch_bounds__(256, (NB <= 4 && (XB || CT != QMM_BF16)) ? 2 : 1) v
 template <int CT, int NB, bool XB>
 hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
     const int64_t grid = a.items * a.c.n_kv * a.chunks;
-    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
-    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    if (grid >= (int64_t(1) << 23)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(64 * kTileRows / wave_rows(CT, NB, XB)), 0,
+                          s, a);
     return e != hipSuccess || !a.splits ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 
@@ -500,8 +564,8 @@ hipError_t tile_x(int xtype, const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Heads of up to 128 values, and wider ones: units of their own, since the
-// first keep accumulators in vector registers and the second need both files.
+// Heads of up to 128 values, and wider ones: units of their own, so that they
+// compile side by side.
 template <int CT>
 hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
