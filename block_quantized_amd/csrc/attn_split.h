@@ -68,6 +68,45 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     const int mr = min(m, rows - 1), mt = mr / heads, head = head0 + mr % heads;
     const int p_row = at.pos + mt;
 
+    // ---- the tiles of this split
+    const int n_pre = (at.pre + 31) >> 5;
+    const int w0 = max(n_pre, at.low >> 5), w1 = (at.end + 31) >> 5;
+    const int n_tiles = n_pre + max(0, w1 - w0);
+    const int per = (n_tiles + w.splits - 1) / w.splits;
+    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
+    const int low_last = a.window > 0 ? at.pos + at.tokens - a.window : INT32_MIN;  // every row sees keys from here
+
+    // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
+    // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page
+    int64_t my_row = -1;
+    int64_t r0[2];
+    int kb = 0;          // first key of the tile last placed
+    bool whole = false;  // every row sees all of its keys
+    auto place = [&](int t) {
+        const int nth = ((t - t0 - wave) / kWaves) & 31;
+        if (nth == 0) {
+            const int tt = t + kWaves * (lane >> 1);
+            const int64_t key = 32 * (int64_t)(tt < n_pre ? tt : tt - n_pre + w0) + 16 * (lane & 1);
+            my_row = -1;
+            if (tt < t1 && key < at.len) {
+                const int pidx = (int)key / a.c.page_size;
+                const int pg = a.c.table[(int64_t)at.s * a.c.table_width + pidx];
+                if (pg >= 0 && pg < a.c.n_pages)
+                    my_row = ((int64_t)pg * a.c.n_kv + kvh) * a.c.page_size + ((int)key - pidx * a.c.page_size);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            r0[u] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, 2 * nth + u) |
+                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
+        kb = 32 * (t < n_pre ? t : t - n_pre + w0);
+        whole = r0[0] >= 0 && r0[1] >= 0 &&
+                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, at.pos + 1)));
+    };
+    // the first lookup is under way while the queries are prepared
+    int t = t0 + wave;
+    if (t < t1) place(t);
+
     // ---- the queries, as B operands in LDS (the waves', one quarter of the
     // blocks written by each): lane (m, g) holds the values 8g..8g+7 of each block
     float qs;  // what a score is multiplied by
@@ -118,14 +157,6 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     if (!(a.softcap > 0.f)) qs *= kLog2e;
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
 
-    // ---- the tiles of this split
-    const int n_pre = (at.pre + 31) >> 5;
-    const int w0 = max(n_pre, at.low >> 5), w1 = (at.end + 31) >> 5;
-    const int n_tiles = n_pre + max(0, w1 - w0);
-    const int per = (n_tiles + w.splits - 1) / w.splits;
-    const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
-    const int low_last = a.window > 0 ? at.pos + at.tokens - a.window : INT32_MIN;  // every row sees keys from here
-
     const int reach = a.window > 0 ? a.window : INT32_MAX;
 
     f4v o[NB][2];
@@ -134,33 +165,6 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     float mx = -INFINITY, mref = 0.f, l = 0.f;  // maximum, the same less 8 or 0, the lane's part of the sum
     float vlim = 0x1p-30f, vinv = 0x1p30f;      // Q8_0: a power of two that no |d| seen is above, and 1 / it
 
-    // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
-    // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page
-    int64_t my_row = -1;
-    int64_t r0[2];
-    int kb = 0;          // first key of the tile last placed
-    bool whole = false;  // every row sees all of its keys
-    auto place = [&](int t) {
-        const int nth = ((t - t0 - wave) / kWaves) & 31;
-        if (nth == 0) {
-            const int tt = t + kWaves * (lane >> 1);
-            const int64_t key = 32 * (int64_t)(tt < n_pre ? tt : tt - n_pre + w0) + 16 * (lane & 1);
-            my_row = -1;
-            if (tt < t1 && key < at.len) {
-                const int pidx = (int)key / a.c.page_size;
-                const int pg = a.c.table[(int64_t)at.s * a.c.table_width + pidx];
-                if (pg >= 0 && pg < a.c.n_pages)
-                    my_row = ((int64_t)pg * a.c.n_kv + kvh) * a.c.page_size + ((int)key - pidx * a.c.page_size);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            r0[u] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, 2 * nth + u) |
-                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
-        kb = 32 * (t < n_pre ? t : t - n_pre + w0);
-        whole = r0[0] >= 0 && r0[1] >= 0 &&
-                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, at.pos + 1)));
-    };
     // whether any row sees the key in half u of the tile: others may hold anything, and count as 0
     auto kept = [&](int u, int key) {
         return (key < at.len) & (r0[u] >= 0) & (((key < at.end) & (key >= at.low)) | (key < at.pre));
@@ -253,11 +257,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
             settle();
         };
         const uint32_t patch = g == 3 ? 0x07060100u : 0x03020100u;
-        int t = t0 + wave;
-        if (t < t1) {
-            place(t);
-            load(a.c.k);
-        }
+        if (t < t1) load(a.c.k);
         for (; t < t1; t += kWaves) {
             stage();
             load(a.c.v);
@@ -381,8 +381,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                         vw[u][i][b] = *reinterpret_cast<const uint32_t*>(vp + voff + 64 * b);
                 }
         };
-        for (int t = t0 + wave; t < t1; t += kWaves) {
-            place(t);
+        for (; t < t1; t += kWaves) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) b0[u] = max(r0[u], (int64_t)0) * RB;
             load_k();
@@ -430,6 +429,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
                     for (int k = PARTS - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
             }
+            place(t + kWaves);
         }
     }
 

@@ -98,8 +98,21 @@ struct Plan {
     int64_t items, parts;
 };
 
+// An upper bound of the keys that a row tile sees, as far as the host knows.
+int64_t key_bound(const qmm_kv_cache* c, const qmm_kv_batch* b) {
+    const int64_t room = (int64_t)b->table_width * c->page_size;
+    return b->max_kv > 0 && b->max_kv < room ? b->max_kv : room;
+}
+
+// Tile kernels multiply 128 rows at a time and split kernels 16, but a tile
+// takes longer to begin and end: they win from 48 rows a sequence on (tokens x
+// query heads of a key-value head; 8 sequences of 1940 keys, 8 heads, Q8_0 and
+// fp32: 31 against 36 us at 32 rows, 48 against 47 at 64, 82 against 58 at
+// 128), and with few keys from as many as make some 10000 products of 16 rows
+// and 32 keys (one sequence: 31 against 36 us at 256 rows, 45 against 40 at 384).
 int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q) {
-    return b->n_tokens * (n_q / c->n_kv) > (int64_t)b->n_seqs * 64 ? 2 : 1;
+    const int64_t rows = up_div(b->n_tokens * (n_q / c->n_kv), b->n_seqs);
+    return rows >= 48 && b->n_seqs * up_div(rows, 16) * c->n_kv * up_div(key_bound(c, b), 32) >= 10000 ? 2 : 1;
 }
 
 Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
@@ -114,17 +127,16 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     while ((2 << p.shift) * p.chunk <= rows && (1 << p.shift) < each) ++p.shift;
     int64_t tiles = (b->n_tokens >> p.shift) + b->n_seqs;  // row tiles at most
     if (tiles > b->n_tokens) tiles = b->n_tokens;
-    int64_t keys = (int64_t)b->table_width * c->page_size;
-    if (b->max_kv > 0 && b->max_kv < keys) keys = b->max_kv;
+    int64_t keys = key_bound(c, b);
     if (o->window > 0 && !o->prefix && o->window + b->n_tokens < keys) keys = o->window + b->n_tokens;
     // The keys are divided among up to 2048 workgroups, more than run at once, so
     // that the last of them end together (64 conversations of 8k to 16k keys: 397 us
     // with 512 workgroups, 362 with 1024, 338 with 2048, 340 with 2560); where that
     // leaves each below 2048 keys, among fewer, at least 512, two a CU (one of
-    // 131k keys, 8 heads: 76 us with 512, 88 with 2048).  A part keeps 256 keys,
-    // two tiles a wave.  Prompts are split only where their row tiles are fewer than
-    // 512.
-    p.least = 8;
+    // 131k keys, 8 heads: 76 us with 512, 88 with 2048).  A part keeps 128 keys, a
+    // tile a wave (one sequence of 1940: 14 us; with 256 keys 16, with 512 22).
+    // Prompts are split only where their row tiles are fewer than 512.
+    p.least = 4;
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
     int64_t s = tiles * keys * heads / 2048;
     s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
