@@ -69,10 +69,11 @@ __global__ void rope_freqs_kernel(double* freqs, int half, double base, double s
 
 // A lane owns four consecutive values of a head, so a head is head_dim / 4
 // lanes of one wavefront and a Q8_0 block 8 of them.  A wavefront takes the
-// heads of one token one after another (q, then k, then v), with the sines
-// and cosines of its lanes' pairs computed once.  The partners of a lane's
-// values are loaded a second time (from L1): the whole head is read before
-// any of it is written, so q_out may be q.
+// heads of one token one after another (q, then k, then v), the next head's
+// loads issued before a head is worked on; the sines and cosines of the token
+// come from LDS, each computed once.  A value's partner is the lane's own
+// (pairs), or loaded a second time (from L1): a whole head is read before any
+// of it is written, so q_out may be q.
 template <int CT, int D, bool BF>
 __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
     constexpr int LPH = D / 4, HPW = 64 / LPH;
@@ -80,109 +81,127 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
     const int heads = a.n_q + 2 * a.c.n_kv;
     const int first = ((int)blockIdx.y * 4 + (int)(threadIdx.x >> 6)) * HPW + hl;
     const int step = (int)gridDim.y * 4 * HPW;
+    // where the partners of the lane's values lie: in the lane itself; four
+    // that follow one another; anywhere (halves of an odd size)
+    const int half = a.n_rot / 2;
+    const bool halves = a.freqs && a.pairing == QMM_ROPE_HALVES, even = half % 4 == 0;
+    const bool turned = a.freqs && e < a.n_rot;
+    const int across = e < half ? e + half : e - half;
 
-    for (int64_t t = blockIdx.x; t < a.c.n_tokens; t += gridDim.x) {
-        const int s = find_seq(a.c, (int)t, a.c.n_seqs + 1);
-        if (s < 0 || s >= a.c.n_seqs) continue;  // a row of no sequence
-        // index of the token in its sequence, and its cache row (-1: none)
-        const int64_t at = (int64_t)a.c.kv_len[s] - clamp_row(a.c.q_start[s + 1], a.c.n_tokens) + t;
-        int64_t row = -1;
-        if (at >= 0 && at / a.c.page_size < a.c.table_width) {
-            const int pg = a.c.table[(int64_t)s * a.c.table_width + at / a.c.page_size];
-            if (pg >= 0 && pg < a.c.n_pages) row = (int64_t)pg * a.c.n_kv * a.c.page_size + at % a.c.page_size;
+    __shared__ double s_cs[128], s_sn[128];
+    const int64_t t = blockIdx.x;
+    const int s = __builtin_amdgcn_readfirstlane(find_seq(a.c, (int)t, a.c.n_seqs + 1));
+    if (s < 0 || s >= a.c.n_seqs) return;  // a row of no sequence
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    // loads the lane's values of the h-th head of the token, and their partners
+    auto load = [&](int h) {
+        if (hl >= HPW || h >= heads) return;
+        const bool isq = h < a.n_q, isv = h >= a.n_q + a.c.n_kv;
+        const void* src = isq ? a.xq : isv ? a.xv : a.xk;
+        const int64_t base = t * (isq ? a.ldq : isv ? a.ldv : a.ldk) +
+                             (int64_t)(isq ? h : isv ? h - a.n_q - a.c.n_kv : h - a.n_q) * D;
+        x = load4<BF>(src, base + e);
+        if (!halves || isv || !turned) return;
+        if (even) {
+            y = load4<BF>(src, base + across);
+        } else {
+            auto partner = [&](int i) { return i >= a.n_rot ? i : i < half ? i + half : i - half; };
+            y.x = load1<BF>(src, base + partner(e)), y.y = load1<BF>(src, base + partner(e + 1));
+            y.z = load1<BF>(src, base + partner(e + 2)), y.w = load1<BF>(src, base + partner(e + 3));
         }
-        double cs[4], sn[4];
-        int partner[4];  // -1: the value is not rotated
-        if (a.freqs) {
+    };
+    load(first);
+    // index of the token in its sequence, and its cache row (-1: none)
+    const int64_t at = (int64_t)a.c.kv_len[s] - clamp_row(a.c.q_start[s + 1], a.c.n_tokens) + t;
+    int64_t row = -1;
+    if (at >= 0 && at < (int64_t)a.c.table_width * a.c.page_size) {  // below 2^30
+        const int nth = (int)at / a.c.page_size;
+        const int pg = a.c.table[(int64_t)s * a.c.table_width + nth];
+        if (pg >= 0 && pg < a.c.n_pages)
+            row = (int64_t)pg * a.c.n_kv * a.c.page_size + ((int)at - nth * a.c.page_size);
+    }
+    // a pair's sine and cosine are computed by one lane for all heads
+    double cs[4], sn[4];  // 1 and 0 where a value stays
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cs[j] = 1.0, sn[j] = 0.0;
+    if (a.freqs) {
+        const int pair = threadIdx.x;
+        if (pair < half) {
+            double p = (double)at;
+            if (a.pos) {
+                const int axis = (pair >= a.bounds[0]) + (pair >= a.bounds[1]) + (pair >= a.bounds[2]);
+                p = (double)a.pos[axis * a.c.n_tokens + t];
+            }
+            sincos64(p * a.freqs[pair], s_sn[pair], s_cs[pair]);
+        }
+        __syncthreads();
+        if (turned) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int half = a.n_rot / 2;
-                int pair = (e + j) >> 1;
-                partner[j] = (e + j) ^ 1;
-                bool upper = j & 1;
-                if (a.pairing == QMM_ROPE_HALVES) {
-                    upper = e + j >= half;
-                    pair = upper ? e + j - half : e + j;
-                    partner[j] = upper ? pair : pair + half;
-                }
-                if (e + j >= a.n_rot) partner[j] = -1;
-                cs[j] = 1.0;
-                sn[j] = 0.0;
-                if (partner[j] >= 0) {
-                    double p = (double)at;
-                    if (a.pos) {
-                        const int axis = (pair >= a.bounds[0]) + (pair >= a.bounds[1]) + (pair >= a.bounds[2]);
-                        p = (double)a.pos[axis * a.c.n_tokens + t];
-                    }
-                    sincos64(p * a.freqs[pair], sn[j], cs[j]);
-                    if (!upper) sn[j] = -sn[j];
-                }
+                const int i = e + j;
+                if (i >= a.n_rot) continue;
+                const int pair = !halves ? i >> 1 : i < half ? i : i - half;
+                cs[j] = s_cs[pair];
+                sn[j] = (halves ? i >= half : j & 1) ? s_sn[pair] : -s_sn[pair];
             }
         }
-        // the loop runs the same number of times in every lane: the maxima of
-        // a Q8_0 block are taken across lanes
-        for (int h0 = 0; h0 < heads; h0 += step) {
-            const int h = h0 + first;
-            const bool on = hl < HPW && h < heads;
-            const bool isq = h < a.n_q, isv = h >= a.n_q + a.c.n_kv;
-            const int kvh = isq ? 0 : isv ? h - a.n_q - a.c.n_kv : h - a.n_q;
-            const void* src = isq ? a.xq : isv ? a.xv : a.xk;
-            const int64_t base = t * (isq ? a.ldq : isv ? a.ldv : a.ldk) + (int64_t)(isq ? h : kvh) * D;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (on) {
-                const float4 w = load4<BF>(src, base + e);
-                x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-                if (a.freqs && !isv) {
-                    float y[4];
+    }
+    // the loop runs the same number of times in every lane: the maxima of
+    // a Q8_0 block are taken across lanes
+    for (int h0 = 0; h0 < heads; h0 += step) {
+        const int h = h0 + first;
+        const bool on = hl < HPW && h < heads;
+        const bool isq = h < a.n_q, isv = h >= a.n_q + a.c.n_kv;
+        const int kvh = isq ? 0 : isv ? h - a.n_q - a.c.n_kv : h - a.n_q;
+        float v[4] = {x.x, x.y, x.z, x.w};
+        if (on && turned && !isv) {
+            const float w[4] = {halves ? y.x : x.y, halves ? y.y : x.x, halves ? y.z : x.w, halves ? y.w : x.z};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = partner[j] >= 0 ? load1<BF>(src, base + partner[j]) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (partner[j] >= 0) x[j] = (float)((double)x[j] * cs[j] + (double)y[j] * sn[j]);
-                }
-            }
-            float d = 0.f, id = 0.f;
-            if constexpr (CT == QMM_Q8_0) {
-                float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-                m = fmaxf(m, __shfl_xor(m, 1));
-                m = fmaxf(m, __shfl_xor(m, 2));
-                m = fmaxf(m, __shfl_xor(m, 4));
-                rtn_scale(m, d, id);
-            }
-            if (!on) continue;
-            if (isq) {
-                const int64_t o = (t * a.n_q + h) * D + e;
-                if constexpr (BF) {
-                    uint2 w;
-                    w.x = f32_bf16(x[0]) | f32_bf16(x[1]) << 16;
-                    w.y = f32_bf16(x[2]) | f32_bf16(x[3]) << 16;
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.q_out) + o) = w;
-                } else {
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + o) = make_float4(x[0], x[1], x[2], x[3]);
-                }
-                continue;
-            }
-            if (row < 0) continue;
-            uint8_t* dst = (isv ? a.c.v : a.c.k) + (row + (int64_t)kvh * a.c.page_size) * kv_row_bytes(CT, D);
-            if constexpr (CT == QMM_Q8_0) {
-                uint8_t* blk = dst + (e >> 5) * kQ8_0Bytes;
-                uint16_t* q = reinterpret_cast<uint16_t*>(blk + 2 + (e & 31));
-                const int c0 = rtn_code(x[0] * id), c1 = rtn_code(x[1] * id), c2 = rtn_code(x[2] * id),
-                          c3 = rtn_code(x[3] * id);
-                q[0] = (uint16_t)((c0 & 0xFF) | (c1 & 0xFF) << 8);
-                q[1] = (uint16_t)((c2 & 0xFF) | (c3 & 0xFF) << 8);
-                if ((e & 31) == 0) *reinterpret_cast<uint16_t*>(blk) = (uint16_t)f2h(d);
-            } else {
+            for (int j = 0; j < 4; ++j)
+                if (e + j < a.n_rot) v[j] = (float)((double)v[j] * cs[j] + (double)w[j] * sn[j]);
+        }
+        load(h + step);
+        float d = 0.f, id = 0.f;
+        if constexpr (CT == QMM_Q8_0) {
+            float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+            m = fmaxf(m, __shfl_xor(m, 1));
+            m = fmaxf(m, __shfl_xor(m, 2));
+            m = fmaxf(m, __shfl_xor(m, 4));
+            rtn_scale(m, d, id);
+        }
+        if (!on) continue;
+        if (isq) {
+            const int64_t o = (t * a.n_q + h) * D + e;
+            if constexpr (BF) {
                 uint2 w;
-                if constexpr (CT == QMM_F16) {
-                    w.x = f2h(x[0]) | f2h(x[1]) << 16;
-                    w.y = f2h(x[2]) | f2h(x[3]) << 16;
-                } else {
-                    w.x = f32_bf16(x[0]) | f32_bf16(x[1]) << 16;
-                    w.y = f32_bf16(x[2]) | f32_bf16(x[3]) << 16;
-                }
-                *reinterpret_cast<uint2*>(dst + 2 * e) = w;
+                w.x = f32_bf16(v[0]) | f32_bf16(v[1]) << 16;
+                w.y = f32_bf16(v[2]) | f32_bf16(v[3]) << 16;
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.q_out) + o) = w;
+            } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + o) = make_float4(v[0], v[1], v[2], v[3]);
             }
+            continue;
+        }
+        if (row < 0) continue;
+        uint8_t* dst = (isv ? a.c.v : a.c.k) + (row + (int64_t)kvh * a.c.page_size) * kv_row_bytes(CT, D);
+        if constexpr (CT == QMM_Q8_0) {
+            uint8_t* blk = dst + (e >> 5) * kQ8_0Bytes;
+            uint16_t* q = reinterpret_cast<uint16_t*>(blk + 2 + (e & 31));
+            const int c0 = rtn_code(v[0] * id), c1 = rtn_code(v[1] * id), c2 = rtn_code(v[2] * id),
+                      c3 = rtn_code(v[3] * id);
+            q[0] = (uint16_t)((c0 & 0xFF) | (c1 & 0xFF) << 8);
+            q[1] = (uint16_t)((c2 & 0xFF) | (c3 & 0xFF) << 8);
+            if ((e & 31) == 0) *reinterpret_cast<uint16_t*>(blk) = (uint16_t)f2h(d);
+        } else {
+            uint2 w;
+            if constexpr (CT == QMM_F16) {
+                w.x = f2h(v[0]) | f2h(v[1]) << 16;
+                w.y = f2h(v[2]) | f2h(v[3]) << 16;
+            } else {
+                w.x = f32_bf16(v[0]) | f32_bf16(v[1]) << 16;
+                w.y = f32_bf16(v[2]) | f32_bf16(v[3]) << 16;
+            }
+            *reinterpret_cast<uint2*>(dst + 2 * e) = w;
         }
     }
 }
@@ -192,7 +211,7 @@ hipError_t append_typed(int xtype, const AppendArgs& a, hipStream_t s) {
     constexpr int HPW = 64 / (D / 4);
     // one token's heads are spread over workgroups while there are few tokens
     const int64_t most = (a.n_q + 2 * a.c.n_kv + 4 * HPW - 1) / (4 * HPW);
-    const int64_t x = a.c.n_tokens < 65536 ? a.c.n_tokens : 65536;
+    const int64_t x = a.c.n_tokens;  // 2^23 at most
     int64_t y = (2048 + x - 1) / x;
     if (y > most) y = most;
     const dim3 grid((unsigned)x, (unsigned)y);
