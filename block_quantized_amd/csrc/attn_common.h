@@ -78,25 +78,29 @@ __device__ __forceinline__ uint2 lds_transpose8(const uint8_t* p) {
     return make_uint2((uint32_t)r.x, (uint32_t)r.y);
 }
 
-// x = cap * tanh(x / cap) * log2 e.  Where every |x / cap| of the wavefront is
-// below 0.35, as scores mostly are, the Taylor series to x^11 (the next term is
-// below 4e-9 x); elsewhere 1 - 2 / (e^2x + 1), which loses bits to
-// cancellation near 0, so that small values keep the series.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&x)[N], float cap, float inv_cap) {
+// x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront
+// is below 0.35, as scores mostly are, the Taylor series to x^11 (the next term
+// is below 4e-9 x; COARSE, for bf16 results: to x^7, below 2e-6 x); elsewhere
+// 1 - 2 / (e^2x + 1), which loses bits to cancellation near 0, so that small
+// values keep the series.
+template <bool COARSE, int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
+    const float in = f / cap, out = cap * kLog2e;
     float big = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i] *= inv_cap;
+        x[i] *= in;
         big = fmaxf(big, fabsf(x[i]));
     }
     const bool large = __any(big >= 0.35f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float x2 = x[i] * x[i];
-        float p = -1382.0f / 155925.0f;
-        p = fmaf(p, x2, 62.0f / 2835.0f);
-        p = fmaf(p, x2, -17.0f / 315.0f);
+        float p = -17.0f / 315.0f;
+        if constexpr (!COARSE) {
+            p = fmaf(-1382.0f / 155925.0f, x2, 62.0f / 2835.0f);
+            p = fmaf(p, x2, -17.0f / 315.0f);
+        }
         p = fmaf(p, x2, 2.0f / 15.0f);
         p = fmaf(p, x2, -1.0f / 3.0f);
         float t = fmaf(p * x2, x[i], x[i]);
@@ -105,7 +109,7 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float cap, float inv_c
             const float u = copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), x[i]);
             t = fabsf(x[i]) < 0.35f ? t : u;
         }
-        x[i] = t * (cap * kLog2e);
+        x[i] = t * out;
     }
 }
 

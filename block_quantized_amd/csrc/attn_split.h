@@ -153,7 +153,6 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         }
     }
     __syncthreads();
-    const float inv_cap = a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
     if (!(a.softcap > 0.f)) qs *= kLog2e;
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
 
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 
     // ---- one tile's scores to P: sc in, p out; raises the running maximum where needed
     auto soften = [&](float (&sc)[8]) {
-        if (a.softcap > 0.f) cap_scores(sc, a.softcap, inv_cap);
+        if (a.softcap > 0.f) cap_scores<false>(sc, 1.0f, a.softcap);
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

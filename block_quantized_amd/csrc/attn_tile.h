@@ -171,7 +171,6 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
     }
     const bool capped = a.softcap > 0.f;
-    const float inv_cap = capped ? 1.0f / a.softcap : 0.f;
     if (!capped) qs *= kLog2e;
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
     const int reach = a.window > 0 ? a.window : INT32_MAX;
@@ -444,12 +443,13 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         for (int j = 0; j < GV; ++j) vf[0][j] = v_operand(j);
         __builtin_amdgcn_sched_barrier(0);
         float f = Q8 ? qs * tile_scale : qs;  // s f: the score, times log2 e without a cap
-        if (capped | (a.slopes != nullptr)) {
+        if (capped) {
+            cap_scores<XB>(s, f, a.softcap);
+            f = 1.0f;
+        }
+        if (a.slopes) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) s[i] *= f;
-            if (capped) cap_scores(s, a.softcap, inv_cap);
-#pragma unroll
-            for (int i = 0; i < R; ++i) s[i] -= slope * fabsf((float)(p_row - (kb + key_of(i))));
+            for (int i = 0; i < R; ++i) s[i] = s[i] * f - slope * fabsf((float)(p_row - (kb + key_of(i))));
             f = 1.0f;
         }
         const bool whole = page[0] && page[1] && page[2] && page[3] &&
