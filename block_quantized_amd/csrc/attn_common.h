@@ -191,7 +191,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
         }
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) all += __shfl_xor(all, k);
-        chunk = max(a.least, (int)(all / (double)a.splits) + 1);
+        chunk = max(a.least, (int)fmin(all / (double)a.splits, 1e9) + 1);
     }
     int base = 0;
     for (int s0 = 0; s0 < n; s0 += 64) {
@@ -228,13 +228,14 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
     return false;
 }
 
-// Where the join finds the parts of a row: part (first + z step) * slots +
-// slot for its splits z.  0 splits: the row is written already.
+// Where the join finds the parts of a row: rows of the workspace, (first + z
+// step) * (rows of an item, all heads) + slot for its splits z.  0 splits: the
+// row is written already.
 struct JoinOf {
     int first, splits, step, slot;
 };
 __device__ __forceinline__ JoinOf* join_of(const AttnArgs& a) {
-    return reinterpret_cast<JoinOf*>(a.work + a.parts * (a.head_dim + 2));
+    return reinterpret_cast<JoinOf*>(a.work + (a.parts * (a.head_dim + 2) + 3) / 4 * 4);
 }
 
 }  // namespace qmm

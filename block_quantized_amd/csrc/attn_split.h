@@ -135,8 +135,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         int ex = 0;
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);  // an all-zero row: any finite scale does
-        const float up = ldexpf(1.0f, 14 - ex);
-        qs = ldexpf(1.0f, ex - 14) * a.scale;
+        constexpr int TOP = BF ? 0 : 14;  // (bf16 parts have fp32's range)
+        const float up = ldexpf(1.0f, TOP - ex);
+        qs = ldexpf(1.0f, ex - TOP) * a.scale;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             if ((b & 3) != wave) continue;
@@ -171,6 +172,10 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 
     // ---- one tile's scores to P: sc in, p out; raises the running maximum where needed
     auto soften = [&](float (&sc)[8]) {
+        if (!whole && a.softcap > 0.f) {  // the scores of masked keys may be anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = kept(i >> 2, kb + 16 * (i >> 2) + 4 * g + (i & 3)) ? sc[i] : 0.f;
+        }
         if (a.softcap > 0.f) cap_scores<false>(sc, 1.0f, a.softcap);
         if (a.slopes) {
 #pragma unroll
@@ -461,9 +466,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         }
         const int64_t row = (int64_t)(at.row + r / heads) * a.n_q + head0 + r % heads;
         if (a.splits && e == 0 && w.split == 0)
-            join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kSplitRows + r};
+            join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * a.slots + r};
         if (w.splits > 1) {
-            const int64_t part = ((int64_t)item * groups + hb) * kSplitRows + r;
+            const int64_t part = ((int64_t)item * groups + hb) * a.slots + r;
             float* ml = a.work + a.parts * D;
             if (e == 0) ml[2 * part] = top, ml[2 * part + 1] = den;
             *reinterpret_cast<f4v*>(a.work + part * D + e) = sum;

@@ -23,7 +23,8 @@
 // are split into two fp16 parts (three bf16 ones for a bf16 cache), and the
 // values of Q8_0 rows, d times a code, into two fp16 parts: three products of
 // parts instead of one.  Q8_0 values are staged times a power of two, the
-// same for all of a tile, that keeps the largest below 2^15.
+// same for all keys of a tile (and one for its values), that keeps the largest
+// below 2^15.
 #pragma once
 
 #include "attn_common.h"
@@ -90,8 +91,8 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     constexpr int BUFS = !Q8 && 2 * (K_BYTES + V_BYTES) * (8 / W) <= 150 * 1024 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) uint8_t s_k[BUFS * AP][K_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t s_v[BUFS * AP][V_BYTES];
-    __shared__ float s_big[2][W];  // of a tile, a wave's keys each: the largest |d| (Q8_0),
-    __shared__ int s_page[2][W];   // and whether they have a page
+    __shared__ float s_big[2][W][2];  // of a tile, a wave's keys each: the largest |d| of K and V (Q8_0),
+    __shared__ int s_page[2][W];      // and whether they have a page
 
     // a long sequence's last tiles see the most keys: they go first.  The
     // heads of a tile are neighbours, so (with 8 of them) each XCD keeps to one
@@ -146,8 +147,9 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);
         // the sign of the scale goes to the queries, and no scale is 0: masked scores stay -inf times it
-        const float up = copysignf(ldexpf(1.0f, 14 - ex), a.scale);
-        qs = fmaxf(ldexpf(1.0f, ex - 14) * fabsf(a.scale), 0x1p-120f);
+        constexpr int TOP = BF ? 0 : 14;  // (bf16 parts have fp32's range)
+        const float up = copysignf(ldexpf(1.0f, TOP - ex), a.scale);
+        qs = fmaxf(ldexpf(1.0f, ex - TOP) * fabsf(a.scale), 0x1p-120f);
 #pragma unroll
         for (int b = 0; b < D / KS; ++b) {
             float x[8];
@@ -197,8 +199,8 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     bool paged = false;
     // key j of the first of the wave's runs of 8 keys in the lanes' order (the second run begins 4 behind it)
     auto nth = [](int j) { return R == 32 ? (j & 3) + 2 * (j & 4) : j; };
-    // Loads the wave's keys of tile t; `big`: the largest |d| of the tile's Q8_0 blocks that this wave holds.
-    auto fetch = [&](int t) -> float {
+    // Loads the wave's keys of tile t; the largest |d| of the Q8_0 blocks of K and V that this lane holds.
+    auto fetch = [&](int t) -> float2 {
         const int from = (t - t0) & 63;
         if (from == 0) {
             const int tt = t + lane;
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         paged = row >= 0;
         const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;  // uniform, with 32-bit offsets of the lanes
         const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
-        float big = 0.f;
+        float2 big = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < St::KT; ++i) {
             const uint32_t task = lane + 64 * i;
@@ -275,17 +277,17 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         if constexpr (Q8) {
 #pragma unroll
             for (int i = 0; i < St::KT; ++i)
-                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB) big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB) big.x = fmaxf(big.x, fabsf(h2f(st.k[i][0])));
 #pragma unroll
             for (int i = 0; i < St::VT; ++i)
                 if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(h2f(st.vd[i][j])));
+                    for (int j = 0; j < 8; ++j) big.y = fmaxf(big.y, fabsf(h2f(st.vd[i][j])));
         }
         return big;
     };
-    // Writes what fetch() loaded to buffer `to`; Q8_0 values times `inv` (a power of two).
-    auto store = [&](float inv, int to) {
+    // Writes what fetch() loaded to buffer `to`; Q8_0 values times powers of two.
+    auto store = [&](float k_inv, float v_inv, int to) {
         uint8_t(*s_kt)[K_BYTES] = s_k + AP * to;
         uint8_t(*s_vt)[V_BYTES] = s_v + AP * to;
 #pragma unroll
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             if constexpr (Q8) {
                 if (KPW * NB % 64 == 0 || task < KPW * NB) {
                     const int key = KPW * wave + task / NB, blk = task % NB;
-                    const float d = h2f(st.k[i][0]) * inv;
+                    const float d = h2f(st.k[i][0]) * k_inv;
                     uint32_t part[16][AP];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 if constexpr (Q8) {
                     float d[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] = h2f(st.vd[i][j]) * inv;
+                    for (int j = 0; j < 8; ++j) d[j] = h2f(st.vd[i][j]) * v_inv;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         u4v w[AP];
@@ -354,12 +356,16 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     };
     // Loads tile t, and tells the other waves about it before the barrier that all pass before store().
     auto begin = [&](int t) {
-        float big = fetch(t);
+        float2 big = fetch(t);
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 1; k < 64; k <<= 1) big = fmaxf(big, __shfl_xor(big, k));
+            for (int k = 1; k < 64; k <<= 1)
+                big.x = fmaxf(big.x, __shfl_xor(big.x, k)), big.y = fmaxf(big.y, __shfl_xor(big.y, k));
         }
-        if (lane == 0) s_big[t & 1][wave] = big, s_page[t & 1][wave] = paged;
+        if (lane == 0) {
+            s_big[t & 1][wave][0] = big.x, s_big[t & 1][wave][1] = big.y;
+            s_page[t & 1][wave] = paged;
+        }
     };
 
     if (t0 < t1) begin(t0);
@@ -368,22 +374,24 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         float tile_scale = 1.0f;
         if constexpr (BUFS == 1) __syncthreads();  // the tile before is multiplied, and this one's s_big told
         if constexpr (Q8) {
-            float big = 0.f;
+            // powers of two, the same in every wave: of this tile's K, and of V so far
+            float bk = 0.f, bv = 0.f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i]);
-            big = fminf(big, 65504.0f);
-            if (big > vlim) {  // the same in every wave
-                int ex;
-                frexpf(big, &ex);
+            for (int i = 0; i < W; ++i) bk = fmaxf(bk, s_big[t & 1][i][0]), bv = fmaxf(bv, s_big[t & 1][i][1]);
+            int ex = 0;
+            frexpf(fminf(bk, 65504.0f), &ex);
+            const float klim = ldexpf(1.0f, ex);
+            if (bv > vlim) {
+                frexpf(fminf(bv, 65504.0f), &ex);
                 const float lim = ldexpf(1.0f, ex), down = vlim / lim;
                 vlim = lim;
 #pragma unroll
                 for (int c = 0; c < NO; ++c) o[c] *= down;
             }
-            tile_scale = vlim * 0x1p-8f;  // values are staged as d code / tile_scale < 2^15
-            store(0x1p8f / vlim, buf);
+            tile_scale = klim * 0x1p-8f;  // values are staged as d code / scale < 2^15
+            store(0x1p8f / klim, 0x1p8f / vlim, buf);
         } else {
-            store(1.0f, buf);
+            store(1.0f, 1.0f, buf);
         }
         __syncthreads();
         bool page[4];  // of each 16 keys
@@ -516,10 +524,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
     const float unit = Q8 ? vlim * 0x1p-8f : 1.0f;
     if (a.splits && h == 0 && w.split == 0)
-        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * kTileRows + R * wave + r};
+        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * a.slots + R * wave + r};
     // accumulator c, value i: value R c + 8 (i / 4) + 4 h + i % 4 of the row
     if (w.splits > 1) {
-        const int64_t part = ((int64_t)item * groups + hb) * kTileRows + R * wave + r;
+        const int64_t part = ((int64_t)item * groups + hb) * a.slots + R * wave + r;
         float* ml = a.work + a.parts * D;
         if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
 #pragma unroll

@@ -94,7 +94,7 @@ int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How qmm_attn divides its work.
 struct Plan {
-    int algo, chunk, chunks, shift, splits, least;
+    int algo, chunk, chunks, shift, splits, least, slots;
     int64_t items, parts;
 };
 
@@ -143,7 +143,8 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     if (s > most) s = most;
     p.splits = keys > 32 * p.least && (p.algo == 1 || s > tiles) ? (int)s : 0;
     p.items = tiles + p.splits;
-    p.parts = p.splits ? p.items * c->n_kv * p.chunks * rows : 0;
+    p.slots = p.chunk << p.shift;
+    p.parts = p.splits ? p.items * heads * p.slots : 0;
     return p;
 }
 
@@ -166,7 +167,8 @@ int check_attn_sizes(const qmm_kv_cache* c, const qmm_kv_batch* b, int xtype, in
 }
 
 size_t work_bytes_of(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q, const Plan& p) {
-    return p.splits ? (size_t)p.parts * (c->head_dim + 2) * 4 + (size_t)b->n_tokens * n_q * 16 : 0;
+    if (!p.splits) return 0;
+    return up_div(p.parts * (c->head_dim + 2) * 4, 16) * 16 + (size_t)b->n_tokens * n_q * 16;
 }
 
 }  // namespace
@@ -274,6 +276,7 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     a.splits = p.splits;
     a.least = p.least;
     a.items = p.items;
+    a.slots = p.slots;
     a.parts = p.parts;
     a.tile_shift = p.shift;
     a.chunk = p.chunk;

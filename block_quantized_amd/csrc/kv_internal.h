@@ -51,7 +51,8 @@ struct AttnArgs {
     int32_t splits;      // parts that the keys of all row tiles are divided in (more or less); 0: not at all
     int32_t least;       // blocks of 32 keys that a part has at least
     int64_t items;       // work items of a head at most
-    int64_t parts;       // rows of the workspace: items x heads x rows of a tile
+    int32_t slots;       // rows of an item at most: tokens of a row tile x chunk
+    int64_t parts;       // rows of the workspace: items x row tiles of heads x slots
 };
 
 // Rows of a row tile: of the split and of the tile kernels.

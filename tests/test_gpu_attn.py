@@ -310,3 +310,129 @@ def test_python_refusals():
         with pytest.raises(Q.QmmError) as e:
             call()
         assert e.value.code == code
+
+
+@pytest.mark.parametrize("algo", (0, 1, 2))
+@pytest.mark.parametrize("cache", [R.Q8, R.BF16])
+def test_many_uneven_sequences(algo, cache):
+    # more sequences than a wavefront looks at together, short ones and none
+    # among them, one long: the keys are divided over all
+    g = synth.rng(41)
+    seqs = [(int(n), int(n) + int(m)) for n, m in zip(g.integers(0, 3, 150), g.integers(0, 40, 150))]
+    seqs[97], seqs[20] = (1, 2500), (9, 700)
+    case = setup(g, seqs, 16, cache, 2, 64)
+    q = R.as_type(synth.normal_f32(g, (case[0].N, 4, 64)), R.F32)
+    run(*case, q, R.F32, 2, 64, algo)
+    b, c, kb, ks, vs = case
+    kb = Q.KVBatch(kb.q_start, kb.kv_len, kb.table, b.N, max_kv=2500)
+    run(b, c, kb, ks, vs, q, R.F32, 2, 64, algo, window=300)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("n_q", [40, 200])
+def test_many_query_heads_of_one(algo, n_q):
+    # more query heads of a key-value head than a row tile holds
+    g = synth.rng(43)
+    case = setup(g, [(1, 50), (5, 300)], 16, R.F16, 1, 64)
+    q = R.as_type(synth.normal_f32(g, (case[0].N, n_q, 64)), R.BF16)
+    run(*case, q, R.BF16, 1, 64, algo, window=170)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("spreads", [(300.0, 1e-3), (1e-3, 300.0)])
+def test_keys_and_values_of_other_sizes(algo, spreads):
+    # Q8_0 scales of keys and values five orders apart, in either direction
+    g = synth.rng(47)
+    b, c, kb, ks, vs = setup(g, [(1, 100), (40, 90)], 16, R.Q8, 1, 64)
+    other = setup(synth.rng(47), [(1, 100), (40, 90)], 16, R.Q8, 1, 64)  # the same pages again
+    for pool, rows, s in ((c.k, ks, spreads[0]), (c.v, vs, spreads[1])):
+        blocks = pool.view(torch.int16).view(*pool.shape[:3], -1, 17)[..., 0].view(torch.float16)
+        blocks.mul_(s)
+        d = blocks.cpu().numpy()
+        for i, L in enumerate(b.len):
+            for j in range(L):
+                row = pool[b.table[i, j // 16], :, j % 16].cpu().numpy()
+                rows[i][j] = R.row_values(row, R.Q8, 64)
+        assert np.isfinite(d).any()
+    q = R.as_type(synth.normal_f32(g, (b.N, 2, 64)) * np.float32(2.0 / spreads[0]), R.F32)
+    run(b, c, kb, ks, vs, q, R.F32, 1, 64, algo)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("cache", [R.Q8, R.F16])
+def test_offsets_past_32_bits(algo, cache):
+    # the same pages at the start and at the end of a pool of over 4 GiB each
+    g = synth.rng(53)
+    n_kv, dim, page = 8, 256, 256
+    per = Q.qmm_kv_bytes(KIND[cache], n_kv, dim, page, 1)
+    n_pages = (1 << 32) // per + 40
+    if torch.cuda.mem_get_info()[0] < 3 * n_pages * per:
+        pytest.skip("not enough free memory")
+    c = Q.KVCache.allocate(KIND[cache], n_kv, dim, page, n_pages)
+    assert c.k.numel() * c.k.element_size() > 1 << 32
+    x = [to_gpu(synth.normal_f32(g, (600, n_kv, dim))) for _ in range(2)]
+    q = to_gpu(synth.normal_f32(g, (600, n_kv, dim)))
+    outs = []
+    for first in (0, n_pages - 3):
+        kb = Q.KVBatch(to_gpu(np.array([0, 600], np.int32)), to_gpu(np.array([600], np.int32)),
+                       to_gpu(np.arange(first, first + 3, dtype=np.int32)[None]), 600)
+        Q.kv_append(c, kb, *x)
+        outs.append(Q.attn(c, kb, q, algo=algo).clone())
+    assert torch.equal(*outs)
+    assert torch.isfinite(outs[0]).all() and outs[0].abs().max() > 0
+    del c
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_lengths_past_the_table(algo):
+    # kv_len beyond the table's pages: the keys behind them do not exist, the
+    # positions count on
+    g = synth.rng(59)
+    b, c, kb, ks, vs = setup(g, [(2, 64)], 16, R.F16, 1, 64, width_more=0)
+    kb = Q.KVBatch(kb.q_start, to_gpu(np.array([80], np.int32)), kb.table, b.N)
+    q = synth.normal_f32(g, (b.N, 1, 64))
+    got = to_cpu(Q.attn(c, kb, to_gpu(q), window=30, algo=algo))
+    for i, p in enumerate((78, 79)):
+        j = np.arange(p - 29, 64)
+        w = np.exp(ks[0][j, 0] @ q[i, 0].astype(np.float64) / 8)
+        want = (w / w.sum()) @ vs[0][j, 0]
+        assert np.linalg.norm(got[i, 0] - want) <= 2.0 ** -18 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_capped_scores_beside_stale_pages(algo):
+    # large scores under a cap in a tile whose rest holds NaNs: the masked
+    # scores must not decide how the others are computed
+    g = synth.rng(61)
+    for cache in (R.Q8, R.F16, R.BF16):
+        case = setup(g, [(1, 5), (3, 21), (1, 70)], 16, cache, 1, 64, spread=6.0)
+        q = R.as_type(synth.normal_f32(g, (case[0].N, 2, 64)), R.F32)
+        run(*case, q, R.F32, 1, 64, algo, softcap=2.0)
+
+
+def test_two_streams_at_once_and_a_captured_prompt():
+    g = synth.rng(67)
+    cases = [setup(g, [(1, 900), (1, 333)], 16, R.Q8, 2, 128), setup(g, [(90, 400)], 32, R.F16, 2, 128)]
+    qs = [to_gpu(synth.normal_f32(g, (c[0].N, 8, 128))) for c in cases]
+    want = [Q.attn(c[1], c[2], q, window=200).clone() for c, q in zip(cases, qs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, (c, q) in enumerate(zip(cases, qs)):
+            got[i].append(Q.attn(c[1], c[2], q, window=200, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+    graph = torch.cuda.CUDAGraph()
+    q = qs[1].clone()
+    with torch.cuda.graph(graph):
+        out = Q.attn(cases[1][1], cases[1][2], q, window=200)
+    for k in (1.0, 0.5, 1.0):
+        q.copy_(qs[1] * k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, Q.attn(cases[1][1], cases[1][2], q, window=200))
+        torch.cuda.synchronize()
+    assert torch.equal(out, want[1])

@@ -1,0 +1,19 @@
+"""The key-value cache's host code (argument validation and planning) under
+AddressSanitizer and UndefinedBehaviorSanitizer, on the CPU: built with g++
+(host code only), the kernel launchers replaced by stand-ins."""
+import os
+import shutil
+
+import pytest
+
+from test_host_sanitizers import FLAGS, OUT, ROOT, SAN, _build_and_run
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_kv_validation_under_sanitizers():
+    exe = os.path.join(OUT, "kv_validation")
+    csrc = os.path.join(ROOT, "block_quantized_amd", "csrc")
+    cmd = ["g++", "-std=c++17", *FLAGS, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", os.path.join(csrc, "kv.cpp"),
+           os.path.join(csrc, "qmm.cpp"), os.path.join(SAN, "abi_stubs.cpp"), os.path.join(SAN, "kv_stubs.cpp"),
+           os.path.join(SAN, "kv_driver.cpp")]
+    assert "kv validation ok" in _build_and_run(cmd, exe)
