@@ -74,7 +74,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     const int n_tiles = n_pre + max(0, w1 - w0);
     const int per = (n_tiles + w.splits - 1) / w.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
-    const int low_last = a.window > 0 ? at.pos + at.tokens - a.window : INT32_MIN;  // every row sees keys from here
+    // every row sees keys from here (no index less a window passes 32 bits from 0 on; rows below it see none)
+    const int low_last = a.window > 0 ? max(at.pos + at.tokens, 0) - a.window : INT32_MIN;
 
     // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
     // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page

@@ -176,8 +176,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     if (!capped) qs *= kLog2e;
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
     const int reach = a.window > 0 ? a.window : INT32_MAX;
-    const int low_last = a.window > 0 ? p_last - a.window + 1 : INT32_MIN;  // every row of the wave sees keys from here
-    const int low_first = a.window > 0 ? p_first - a.window + 1 : INT32_MIN;
+    // every row of the wave sees keys from low_last on, and one from low_first (no index less a window passes 32
+    // bits from 0 on; rows below it see none)
+    const int low_last = a.window > 0 ? max(p_last, 0) - a.window + 1 : INT32_MIN;
+    const int low_first = a.window > 0 ? max(p_first, 0) - a.window + 1 : INT32_MIN;
 
     // ---- the tiles of this split
     const int n_pre = (at.pre + kKeys - 1) / kKeys;

@@ -436,3 +436,13 @@ def test_two_streams_at_once_and_a_captured_prompt():
         assert torch.equal(out, Q.attn(cases[1][1], cases[1][2], q, window=200))
         torch.cuda.synchronize()
     assert torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("cache", [R.Q8, R.F16])
+def test_largest_window_and_tokens_before_the_first(algo, cache):
+    # an index below 0 less a window of 2^31 - 1 passes 32 bits
+    g = synth.rng(30)
+    b, c, kb, ks, vs = setup(g, [(40, 25), (3, 2), (70, 69)], 16, cache, 1, 64)
+    q = synth.normal_f32(g, (b.N, 2, 64))
+    run(b, c, kb, ks, vs, q, R.F32, 1, 64, algo, window=2 ** 31 - 1)
