@@ -82,7 +82,6 @@ hipError_t join_x(int xtype, const AttnArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    if (a.c.n_tokens * a.n_q >= (int64_t(1) << 30)) return hipErrorInvalidConfiguration;  // 2^32 work-items
     switch (head_dim) {
     case 64: return join_x<64>(xtype, a, s);
     case 96: return join_x<96>(xtype, a, s);

@@ -491,8 +491,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 
 template <int CT, int NB, bool XB>
 hipError_t split_typed(const AttnArgs& a, hipStream_t s) {
-    const int64_t grid = a.items * a.c.n_kv * a.chunks;
-    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    const int64_t grid = a.items * a.c.n_kv * a.chunks;  // below 2^32 work-items
     hipError_t e = launch(attn_split_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(256), 0, s, a);
     if (e != hipSuccess || !a.splits) return e;
     return launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);

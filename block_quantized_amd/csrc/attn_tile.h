@@ -560,8 +560,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 
 template <int CT, int NB, bool XB>
 hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
-    const int64_t grid = a.items * a.c.n_kv * a.chunks;
-    if (grid >= (int64_t(1) << 23)) return hipErrorInvalidConfiguration;  // 2^32 work-items
+    const int64_t grid = a.items * a.c.n_kv * a.chunks;  // below 2^32 work-items
     hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(64 * kTileRows / wave_rows(CT, NB, XB)), 0,
                           s, a);
     return e != hipSuccess || !a.splits ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);

@@ -12,8 +12,9 @@ using namespace qmm;
 
 namespace {
 
-constexpr int64_t kMaxRows = int64_t(1) << 23;     // tokens + sequences: grids stay below 2^32 work-items
+constexpr int64_t kMaxRows = (int64_t(1) << 23) - 1;  // tokens: grids stay below 2^32 work-items
 constexpr int64_t kMaxLength = int64_t(1) << 30;   // tokens of a sequence
+constexpr int kMaxSeqs = 1 << 16;                  // every workgroup looks its sequence up among them
 constexpr int kMaxHeads = 4096;
 
 int hip_status(hipError_t e) { return e == hipSuccess ? QMM_OK : QMM_ERR_HIP; }
@@ -55,7 +56,7 @@ int check_cache(const qmm_kv_cache* c) {
 int check_batch_sizes(const qmm_kv_cache* c, const qmm_kv_batch* b) {
     if (!b) return QMM_ERR_NULL;
     if (b->n_seqs <= 0 || b->table_width <= 0 || b->n_tokens <= 0 || b->max_kv < 0) return QMM_ERR_SHAPE;
-    if (b->n_tokens > kMaxRows || b->n_tokens + b->n_seqs > kMaxRows) return QMM_ERR_SHAPE;
+    if (b->n_tokens > kMaxRows || b->n_seqs > kMaxSeqs) return QMM_ERR_SHAPE;
     if ((int64_t)b->table_width * c->page_size > kMaxLength) return QMM_ERR_SHAPE;
     return QMM_OK;
 }
@@ -138,7 +139,7 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     // Prompts are split only where their row tiles are fewer than 512.
     p.least = 4;
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
-    int64_t s = tiles * keys * heads / 2048;
+    int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
     s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
     if (s > most) s = most;
     p.splits = keys > 32 * p.least && (p.algo == 1 || s > tiles) ? (int)s : 0;
@@ -146,6 +147,12 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     p.slots = p.chunk << p.shift;
     p.parts = p.splits ? p.items * heads * p.slots : 0;
     return p;
+}
+
+// Whether the grids of qmm_attn stay below 2^32 work-items.
+bool fits(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q, const Plan& p) {
+    return p.items * c->n_kv * p.chunks < int64_t(1) << (p.algo == 2 ? 23 : 24) &&
+           (!p.splits || b->n_tokens * n_q < int64_t(1) << 30);
 }
 
 int check_opts(const qmm_attn_opts* o) {
@@ -239,13 +246,17 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
 }
 
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q) {
-    return check_attn_sizes(cache, batch, xtype, n_q) ? 0 : choose(cache, batch, n_q);
+    if (check_attn_sizes(cache, batch, xtype, n_q)) return 0;
+    const qmm_attn_opts none = {};
+    const Plan p = plan(cache, batch, &none, n_q);
+    return fits(cache, batch, n_q, p) ? p.algo : 0;
 }
 
 size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
                      int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
-    return work_bytes_of(cache, batch, n_q, plan(cache, batch, opts, n_q));
+    const Plan p = plan(cache, batch, opts, n_q);
+    return fits(cache, batch, n_q, p) ? work_bytes_of(cache, batch, n_q, p) : 0;
 }
 
 int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,
@@ -255,6 +266,7 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     if ((rc = check_attn_sizes(cache, batch, xtype, n_q)) || (rc = check_opts(opts))) return rc;
     if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, cache->head_dim)) || (rc = check_ptr(out))) return rc;
     const Plan p = plan(cache, batch, opts, n_q);
+    if (!fits(cache, batch, n_q, p)) return QMM_ERR_SHAPE;
     const size_t need = work_bytes_of(cache, batch, n_q, p);
     if (need) {
         if ((rc = check_ptr(work))) return rc;

@@ -9,7 +9,9 @@
  * 16-bit floats.  The conventions of qmm.h hold for every call: the caller
  * owns every buffer, nothing is allocated, copied to the host or
  * synchronized, work is enqueued on `stream`, arguments are checked before
- * anything is enqueued, and the status codes are qmm.h's.
+ * anything is enqueued, and the status codes are qmm.h's.  Arrays of 32-bit
+ * values are 4-byte aligned, the angles of a rotation 8-byte; every other
+ * device pointer 16-byte (QMM_ERR_ALIGN otherwise).
  *
  * What lies in device memory cannot be checked on the host.  The kernels
  * check it themselves: no read or write leaves the buffers for any contents
@@ -61,9 +63,9 @@ typedef struct {
     const int32_t* q_start; /* device, n_seqs + 1, not decreasing, first 0     */
     const int32_t* kv_len;  /* device, n_seqs                                  */
     const int32_t* table;   /* device, n_seqs x table_width                    */
-    int32_t n_seqs;
-    int32_t table_width;    /* pages of a sequence at most                     */
-    int64_t n_tokens;       /* rows of q, k, v and out                         */
+    int32_t n_seqs;         /* 65536 at most                                   */
+    int32_t table_width;    /* pages of a sequence at most, 2^30 tokens in all */
+    int64_t n_tokens;       /* rows of q, k, v and out, below 2^23             */
     int64_t max_kv;         /* largest kv_len, as far as known; 0: unknown.  It
                                only decides how the work is split: results hold
                                for any value                                   */
@@ -141,7 +143,8 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
  *           same time need one each; contents need not be kept.
  * Fp32 results are as exact as a product in fp32.  What lies in the cache at
  * places that no row of the call sees has no effect, infinities and NaN
- * included; visible keys and values have to be finite. */
+ * included; visible keys and values have to be finite.  Batches whose grids
+ * would pass 2^32 work-items are refused (QMM_ERR_SHAPE). */
 int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,
              int64_t ldq, int n_q, void* out, void* work, size_t work_bytes, void* stream);
 

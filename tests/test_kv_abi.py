@@ -65,7 +65,8 @@ GEOMETRY = [
     (dict(b=batch(n_seqs=0)), Q.QMM_ERR_SHAPE), (dict(b=batch(n_tokens=0)), Q.QMM_ERR_SHAPE),
     (dict(b=batch(table_width=0)), Q.QMM_ERR_SHAPE), (dict(b=batch(table_width=2 ** 30)), Q.QMM_ERR_SHAPE),
     (dict(b=batch(max_kv=-1)), Q.QMM_ERR_SHAPE), (dict(b=batch(n_tokens=2 ** 31)), Q.QMM_ERR_SHAPE),
-    (dict(b=batch(n_seqs=2 ** 30)), Q.QMM_ERR_SHAPE),
+    (dict(b=batch(n_seqs=2 ** 30)), Q.QMM_ERR_SHAPE), (dict(b=batch(n_seqs=2 ** 16 + 1)), Q.QMM_ERR_SHAPE),
+    (dict(b=batch(n_tokens=2 ** 23)), Q.QMM_ERR_SHAPE),
     (dict(b=batch(q_start=None)), Q.QMM_ERR_NULL), (dict(b=batch(kv_len=A + 2)), Q.QMM_ERR_ALIGN),
     (dict(b=batch(table=None)), Q.QMM_ERR_NULL),
     (dict(q=A + 4), Q.QMM_ERR_ALIGN), (dict(ldq=508), Q.QMM_ERR_SHAPE), (dict(ldq=504), Q.QMM_ERR_SHAPE),
@@ -128,6 +129,20 @@ def test_choice():
     assert Q.qmm_attn_choice(cache(), batch(), Q.QMM_F32, 3) == 0
     assert Q.qmm_attn_choice(cache(), batch(), Q.QMM_F16, 4) == 0
     assert Q.qmm_attn_choice(cache(page_size=15), batch(), Q.QMM_F32, 4) == 0
+
+
+def test_grids_of_too_many_workgroups():
+    # 2^23 - 1 single rows of 512 heads, in row tiles of 16 (split) or 128 (tile kernels)
+    c, b = cache(n_kv=512), batch(n_tokens=2 ** 23 - 1, n_seqs=1, table_width=4)
+    for algo in (0, 1, 2):
+        o = opts(algo=algo)
+        assert Q.qmm_attn_work(c, b, o, Q.QMM_F32, 512) == 0
+        assert attn(c=c, b=b, o=o, n_q=512, ldq=512 * 128) == Q.QMM_ERR_SHAPE
+    assert Q.qmm_attn_choice(c, b, Q.QMM_F32, 512) == 0
+    # the largest sizes of all leave no product past 64 bits behind
+    c = cache(n_kv=4096, page_size=2 ** 20, n_pages=1)
+    assert Q.qmm_attn_work(c, batch(n_tokens=2 ** 23 - 1, n_seqs=2 ** 16, table_width=2 ** 10), opts(algo=1), Q.QMM_F32,
+                           4096) == 0
 
 
 def test_rope_freqs_refusals():
