@@ -336,7 +336,7 @@ class KVCache:
 
     def __init__(self, k, v, type: int, n_kv: int, head_dim: int, page_size: int):
         page = qmm_kv_bytes(type, n_kv, head_dim, page_size, 1)
-        if not page:
+        if not page or max(type, n_kv, head_dim, page_size) >= 1 << 31:  # (ctypes took their low 32 bits)
             _refuse(QMM_ERR_UNSUPPORTED, "KVCache: type, heads, head_dim or page_size")
         size = k.numel() * k.element_size()
         if size != v.numel() * v.element_size() or not size or size % page:
@@ -367,6 +367,9 @@ class KVBatch:
 
     def __init__(self, q_start, kv_len, table, n_tokens: int, max_kv: int = 0):
         n = kv_len.numel()
+        if not 0 < n_tokens < 1 << 23 or max_kv < 0:
+            _refuse(QMM_ERR_SHAPE, "KVBatch: n_tokens has to be 1 to 2^23 - 1, max_kv 0 or more")
+        max_kv = min(max_kv, 1 << 30)
         _int32("KVBatch: kv_len", kv_len, n)
         _int32("KVBatch: q_start", q_start, n + 1)
         if table.dim() != 2:
@@ -393,6 +396,8 @@ class Rope:
         if pos is not None:
             if pos.dim() == 1:
                 pos = pos[None]
+            if pos.dim() != 2:
+                _refuse(QMM_ERR_SHAPE, "Rope: pos has to be axes x tokens")
             _int32("Rope: pos", pos, axes, pos.shape[1])
         self.dev = _device_of("Rope", freqs, pos)
         self.freqs, self.pos = freqs, pos
@@ -413,6 +418,8 @@ def rope_freqs(n_rot: int, base: float, scale: float = 1.0, factors=None, device
     if factors is not None and (factors.dtype != torch.float32 or factors.numel() != n_rot // 2
                                 or not factors.is_contiguous()):
         _refuse(QMM_ERR_SHAPE, "rope_freqs: factors have to be n_rot / 2 contiguous float32 values")
+    if not 0 < n_rot <= 65536:
+        _refuse(QMM_ERR_SHAPE, "rope_freqs: n_rot has to be 2 to 65536")
     handle, where = _elsewhere(index, stream)
     with where:
         freqs = torch.empty(max(n_rot // 2, 1), dtype=torch.float64, device=torch.device("cuda", index))
@@ -514,6 +521,8 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
         same = same and prefix.get_device() == dev
     if not same:
         _refuse(QMM_ERR_UNSUPPORTED, "attn: tensors have to lie on one GPU, and out be of q's type")
+    if not 0 <= window < 1 << 31 or not 0 <= algo <= 2:  # ctypes would take their low 32 bits
+        _refuse(QMM_ERR_UNSUPPORTED, "attn: window has to be 0 to 2^31 - 1, algo 0 to 2")
     xtype = _xtype("attn", dtype)
     opts = ctypes.byref(qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes),
                                       _ptr(prefix)))

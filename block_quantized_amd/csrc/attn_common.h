@@ -70,14 +70,6 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
                codes_f16(hi, 0x04030402u)};
 }
 
-// Eight rows of 16 bytes in LDS, transposed: of 16 lanes, lane i points at 8
-// bytes (8-byte aligned), half i % 2 of row i / 2, and gets byte i of each row.
-__device__ __forceinline__ uint2 lds_transpose8(const uint8_t* p) {
-    typedef int i2v __attribute__((ext_vector_type(2)));
-    const i2v r = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i2v*)p);
-    return make_uint2((uint32_t)r.x, (uint32_t)r.y);
-}
-
 // x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront
 // is below 0.35, as scores mostly are, the Taylor series to x^11 (the next term
 // is below 4e-9 x; COARSE, for bf16 results: to x^7, below 2e-6 x); elsewhere

@@ -67,9 +67,9 @@ struct Staged {
     uint32_t vd[VT][Q8 ? 8 : 1];
 };
 
-// Parts of Q and P, and rows of a wave.
 // The largest group of operands, up to `most`, that n of them divide into.
 constexpr int group_of(int n, int most) { return n % most ? group_of(n, most - 1) : most; }
+// Parts of Q and P, and rows of a wave.
 constexpr int q_parts(int ct, bool xb) { return xb ? 1 : ct == QMM_BF16 ? 3 : 2; }
 constexpr int wave_rows(int ct, int nb, bool xb) { return nb > 4 || q_parts(ct, xb) == 3 ? 16 : 32; }
 

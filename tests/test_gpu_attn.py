@@ -446,3 +446,15 @@ def test_largest_window_and_tokens_before_the_first(algo, cache):
     b, c, kb, ks, vs = setup(g, [(40, 25), (3, 2), (70, 69)], 16, cache, 1, 64)
     q = synth.normal_f32(g, (b.N, 2, 64))
     run(b, c, kb, ks, vs, q, R.F32, 1, 64, algo, window=2 ** 31 - 1)
+
+
+def test_python_refuses_what_ctypes_would_cut():
+    g = synth.rng(31)
+    b, c, kb, ks, vs = setup(g, [(2, 9)], 16, R.F16, 2, 64)
+    q = torch.zeros(2, 4, 64, device="cuda")
+    for options in (dict(window=2 ** 31), dict(window=2 ** 32 + 5), dict(window=-1), dict(algo=3), dict(algo=2 ** 32 + 1)):
+        with pytest.raises(Q.QmmError) as e:
+            Q.attn(c, kb, q, **options)
+        assert e.value.code == Q.QMM_ERR_UNSUPPORTED
+    with pytest.raises(Q.QmmError):
+        Q.rope_freqs(2 ** 32 + 64, 1e4)

@@ -167,7 +167,14 @@ def test_holders_refuse_cpu_tensors_and_shapes():
                        (lambda: Q.KVCache(torch.zeros(9), torch.zeros(9), Q.QMM_F16, 1, 64, 16), Q.QMM_ERR_SHAPE),
                        (lambda: Q.Rope(torch.zeros(4), 0), Q.QMM_ERR_SHAPE),
                        (lambda: Q.Rope(torch.zeros(4, dtype=torch.float64), 0, sections=[1] * 5), Q.QMM_ERR_SHAPE),
-                       (lambda: Q.Rope(torch.zeros(4, dtype=torch.float64), 0, pos=i(2, 3)), Q.QMM_ERR_SHAPE)):
+                       (lambda: Q.Rope(torch.zeros(4, dtype=torch.float64), 0, pos=i(2, 3)), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.Rope(torch.zeros(4, dtype=torch.float64), 0, pos=i(1)[0]), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.Rope(torch.zeros(4, dtype=torch.float64), 0, pos=i(1, 1, 3)), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.KVBatch(i(3), i(2), i(2, 2), 0), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.KVBatch(i(3), i(2), i(2, 2), 2 ** 23), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.KVBatch(i(3), i(2), i(2, 2), 2, max_kv=-1), Q.QMM_ERR_SHAPE),
+                       (lambda: Q.KVCache(torch.zeros(1088), torch.zeros(1088), Q.QMM_Q8_0, 1, 64, 2 ** 32 + 16),
+                        Q.QMM_ERR_UNSUPPORTED)):
         with pytest.raises(Q.QmmError) as e:
             make()
         assert e.value.code == code
