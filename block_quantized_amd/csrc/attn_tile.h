@@ -198,11 +198,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 
     int64_t my_row = -1;  // lane i: where the wave's keys of tile i from here on begin in the cache, or -1
     St st;
-    bool paged = false;
     // key j of the first of the wave's runs of 8 keys in the lanes' order (the second run begins 4 behind it)
     auto nth = [](int j) { return R == 32 ? (j & 3) + 2 * (j & 4) : j; };
-    // Loads the wave's keys of tile t; the largest |d| of the Q8_0 blocks of K and V that this lane holds.
-    auto fetch = [&](int t) -> float2 {
+    // Where the wave's keys of tile t begin in the cache, or -1.
+    auto row_of = [&](int t) -> int64_t {
         const int from = (t - t0) & 63;
         if (from == 0) {
             const int tt = t + lane;
@@ -215,10 +214,22 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                     my_row = ((int64_t)pg * a.c.n_kv + kvh) * a.c.page_size + ((int)key - pidx * a.c.page_size);
             }
         }
-        const int64_t row = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, from) |
-                                      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from) << 32);
-        const int key0 = kKeys * (t < n_pre ? t : t - n_pre + w0) + KPW * wave;
-        paged = row >= 0;
+        return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_row, from) |
+                         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), from) << 32);
+    };
+    // Whether a key of the wave's in tile t, at cache row `row`, is seen by any row of the tile: others may hold
+    // anything, and count as 0.
+    auto key_at = [&](int t) { return kKeys * (t < n_pre ? t : t - n_pre + w0) + KPW * wave; };
+    auto all_kept = [&](int64_t row, int key0) {
+        return (row >= 0) & ((key0 + KPW <= at.pre) | ((key0 >= at.low) & (key0 + KPW <= at.end)));
+    };
+    auto kept = [&](int64_t row, int key) {
+        return (row >= 0) & (((key >= at.low) & (key < at.end)) | (key < at.pre));
+    };
+    // Loads the wave's keys and values of tile t, which begin at cache row `row`; the largest |d| of the Q8_0 blocks of K
+    // and of V that this lane holds.
+    auto fetch = [&](int t, int64_t row) -> float2 {
+        const int key0 = key_at(t);
         const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;  // uniform, with 32-bit offsets of the lanes
         const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
         float2 big = make_float2(0.f, 0.f);
@@ -252,15 +263,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 }
             }
         }
-        // a key that no row sees may hold anything: it counts as 0
-        if (!(paged & ((key0 + KPW <= at.pre) | ((key0 >= at.low) & (key0 + KPW <= at.end))))) {
-            auto kept = [&](int key) {
-                key += key0;
-                return paged & (((key >= at.low) & (key < at.end)) | (key < at.pre));
-            };
+        if (!all_kept(row, key0)) {
 #pragma unroll
             for (int i = 0; i < St::KT; ++i) {
-                const bool ok = kept((lane + 64 * i) / (Q8 ? NB : 4 * NB));
+                const bool ok = kept(row, key0 + (lane + 64 * i) / (Q8 ? NB : 4 * NB));
 #pragma unroll
                 for (int j = 0; j < (Q8 ? 1 : 4); ++j) st.k[i][j] = ok ? st.k[i][j] : 0;
             }
@@ -268,7 +274,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             for (int i = 0; i < St::VT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const bool ok = kept(4 * ((lane + 64 * i) / (8 * NB)) + nth(j));
+                    const bool ok = kept(row, key0 + 4 * ((lane + 64 * i) / (8 * NB)) + nth(j));
                     if constexpr (Q8) {
                         st.vd[i][j] = ok ? st.vd[i][j] : 0;
                     } else {
@@ -288,10 +294,9 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
         return big;
     };
-    // Writes what fetch() loaded to buffer `to`; Q8_0 values times powers of two.
-    auto store = [&](float k_inv, float v_inv, int to) {
+    // Write what was fetched to buffer `to`; Q8_0 values times powers of two.
+    auto store_k = [&](float k_inv, int to) {
         uint8_t(*s_kt)[K_BYTES] = s_k + AP * to;
-        uint8_t(*s_vt)[V_BYTES] = s_v + AP * to;
 #pragma unroll
         for (int i = 0; i < St::KT; ++i) {
             const int task = lane + 64 * i;
@@ -318,6 +323,9 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 *reinterpret_cast<u4v*>(&s_kt[0][k_at(key, c)]) = u4v{st.k[i][0], st.k[i][1], st.k[i][2], st.k[i][3]};
             }
         }
+    };
+    auto store_v = [&](float v_inv, int to) {
+        uint8_t(*s_vt)[V_BYTES] = s_v + AP * to;
 #pragma unroll
         for (int i = 0; i < St::VT; ++i) {
             const int task = lane + 64 * i;
@@ -356,9 +364,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             }
         }
     };
-    // Loads tile t, and tells the other waves about it before the barrier that all pass before store().
+    // Loads tile t, and tells the other waves about it before the barrier that all pass before it is stored.
     auto begin = [&](int t) {
-        float2 big = fetch(t);
+        const int64_t row = row_of(t);
+        float2 big = fetch(t, row);
         if constexpr (Q8) {
 #pragma unroll
             for (int k = 1; k < 64; k <<= 1)
@@ -366,93 +375,54 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
         if (lane == 0) {
             s_big[t & 1][wave][0] = big.x, s_big[t & 1][wave][1] = big.y;
-            s_page[t & 1][wave] = paged;
+            s_page[t & 1][wave] = row >= 0;
+        }
+    };
+    // Q8_0: powers of two, the same in every wave, of tile t's K (the limit is
+    // returned), and of V so far (vlim: raised where tile t needs it, o with it).
+    // Values are staged as 2^8 d code / limit < 2^15.
+    auto k_limit = [&](int t) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i][0]);
+        int ex = 0;
+        frexpf(fminf(big, 65504.0f), &ex);
+        return ldexpf(1.0f, ex);
+    };
+    auto v_limit = [&](int t) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i][1]);
+        if (big > vlim) {
+            int ex = 0;
+            frexpf(fminf(big, 65504.0f), &ex);
+            const float lim = ldexpf(1.0f, ex), down = vlim / lim;
+            vlim = lim;
+#pragma unroll
+            for (int c = 0; c < NO; ++c) o[c] *= down;
         }
     };
 
-    if (t0 < t1) begin(t0);
-    for (int t = t0; t < t1; ++t) {
-        const int buf = BUFS > 1 ? t & 1 : 0;
-        float tile_scale = 1.0f;
-        if constexpr (BUFS == 1) __syncthreads();  // the tile before is multiplied, and this one's s_big told
-        if constexpr (Q8) {
-            // powers of two, the same in every wave: of this tile's K, and of V so far
-            float bk = 0.f, bv = 0.f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) bk = fmaxf(bk, s_big[t & 1][i][0]), bv = fmaxf(bv, s_big[t & 1][i][1]);
-            int ex = 0;
-            frexpf(fminf(bk, 65504.0f), &ex);
-            const float klim = ldexpf(1.0f, ex);
-            if (bv > vlim) {
-                frexpf(fminf(bv, 65504.0f), &ex);
-                const float lim = ldexpf(1.0f, ex), down = vlim / lim;
-                vlim = lim;
-#pragma unroll
-                for (int c = 0; c < NO; ++c) o[c] *= down;
-            }
-            tile_scale = klim * 0x1p-8f;  // values are staged as d code / scale < 2^15
-            store(0x1p8f / klim, 0x1p8f / vlim, buf);
-        } else {
-            store(1.0f, 1.0f, buf);
-        }
-        __syncthreads();
+    constexpr int STEPS = D / KS, SUBS = kKeys / R;  // of an accumulator's products, accumulators of scores
+    constexpr int NK = SUBS * AP * STEPS, NV = kKeys / KS * NO * AP;  // A operands of a tile: of K and of V
+    // operand i of K: (keys, part, values); of V: (step, values, part)
+    auto k_operand = [&](int buf, int i) {
+        const int u = i / (STEPS * AP), ap = AP - 1 - i / STEPS % AP, b = i % STEPS;
+        const int key = R == 32 ? 32 * u + r : 32 * (u >> 1) + 8 * (r >> 2) + 4 * (u & 1) + (r & 3);
+        return *reinterpret_cast<const u4v*>(&s_k[AP * buf + ap][k_at(key, GROUPS * b + h)]);
+    };
+    auto v_operand = [&](int buf, int i) {
+        const int kk = i / (NO * AP), c = i / AP % NO, ap = AP - 1 - i % AP, dim = R * c + r;
+        return *reinterpret_cast<const u4v*>(&s_v[AP * buf + ap][dim * (2 * kKeys) + 16 * v_slot(dim, GROUPS * kk + h)]);
+    };
+    float s[R];
+    // From the products of tile t to scores (f s, times log2 e), masked; raises
+    // the running maximum where they pass it by 2^7.
+    auto soften = [&](int t, float& f) {
+        const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
         bool page[4];  // of each 16 keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) page[i] = s_page[t & 1][W / 4 * i] != 0;
-        const uint8_t(*s_kt)[K_BYTES] = s_k + AP * buf;
-        const uint8_t(*s_vt)[V_BYTES] = s_v + AP * buf;
-        if (t + 1 < t1) begin(t + 1);
-
-        const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
-        // nothing of this tile for any row of the wave
-        if (idle || !((kb < at.pre) || (kb <= p_last && kb < at.len && kb + kKeys - 1 >= low_first))) continue;
-        // Operands come from LDS some at a time, the next ones while these are
-        // multiplied: left to itself the compiler waits for each before its use.
-        constexpr int STEPS = D / KS, SUBS = kKeys / R;  // of an accumulator's products, accumulators of scores
-        constexpr int GK = group_of(SUBS * AP * STEPS, BP > 1 ? 2 : 4), GV = group_of(NO * AP, BP > 1 ? 2 : 4);
-        float s[R];
-        {
-            accv acc[SUBS];
-#pragma unroll
-            for (int u = 0; u < SUBS; ++u)
-#pragma unroll
-                for (int i = 0; i < VL; ++i) acc[u][i] = 0.f;
-            constexpr int N = SUBS * AP * STEPS;  // (keys, part, values)
-            auto operand = [&](int i) {
-                const int u = i / (STEPS * AP), ap = AP - 1 - i / STEPS % AP, b = i % STEPS;
-                const int key = R == 32 ? 32 * u + r : 32 * (u >> 1) + 8 * (r >> 2) + 4 * (u & 1) + (r & 3);
-                return *reinterpret_cast<const u4v*>(&s_kt[ap][k_at(key, GROUPS * b + h)]);
-            };
-            u4v kf[2][GK];
-#pragma unroll
-            for (int j = 0; j < GK; ++j) kf[0][j] = operand(j);
-#pragma unroll
-            for (int i = 0; i < N; i += GK) {
-                if (i + GK < N) {
-#pragma unroll
-                    for (int j = 0; j < GK; ++j) kf[(i / GK + 1) & 1][j] = operand(i + GK + j);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int j = 0; j < GK; ++j) {
-                    const int u = (i + j) / (STEPS * AP), ap = AP - 1 - (i + j) / STEPS % AP, b = (i + j) % STEPS;
-#pragma unroll
-                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) acc[u] = mfma_of<BF>(kf[(i / GK) & 1][j], qf[b][k], acc[u]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i) s[i] = acc[i / VL][i % VL];
-        }
-        auto v_operand = [&](int i) {  // (step, values, part)
-            const int kk = i / (NO * AP), c = i / AP % NO, ap = AP - 1 - i % AP, dim = R * c + r;
-            return *reinterpret_cast<const u4v*>(&s_vt[ap][dim * (2 * kKeys) + 16 * v_slot(dim, GROUPS * kk + h)]);
-        };
-        u4v vf[2][GV];
-#pragma unroll
-        for (int j = 0; j < GV; ++j) vf[0][j] = v_operand(j);
-        __builtin_amdgcn_sched_barrier(0);
-        float f = Q8 ? qs * tile_scale : qs;  // s f: the score, times log2 e without a cap
         if (capped) {
             cap_scores<XB>(s, f, a.softcap);
             f = 1.0f;
@@ -488,6 +458,64 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 #pragma unroll
             for (int c = 0; c < NO; ++c) o[c] *= down;
         }
+    };
+
+    if (t0 < t1) begin(t0);
+    for (int t = t0; t < t1; ++t) {
+        const int buf = BUFS > 1 ? t & 1 : 0;
+        float f = qs;
+        if constexpr (BUFS == 1) __syncthreads();  // the tile before is multiplied, and this one's s_big told
+        if constexpr (Q8) {
+            const float lim = k_limit(t);
+            v_limit(t);
+            f *= lim * 0x1p-8f;
+            store_k(0x1p8f / lim, buf);
+            store_v(0x1p8f / vlim, buf);
+        } else {
+            store_k(1.0f, buf);
+            store_v(1.0f, buf);
+        }
+        __syncthreads();
+        if (t + 1 < t1) begin(t + 1);
+
+        const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
+        // nothing of this tile for any row of the wave
+        if (idle || !((kb < at.pre) || (kb <= p_last && kb < at.len && kb + kKeys - 1 >= low_first))) continue;
+        // Operands come from LDS some at a time, the next ones while these are
+        // multiplied: left to itself the compiler waits for each before its use.
+        constexpr int GK = group_of(NK, BP > 1 ? 2 : 4), GV = group_of(NO * AP, BP > 1 ? 2 : 4);
+        {
+            accv acc[SUBS];
+#pragma unroll
+            for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+                for (int i = 0; i < VL; ++i) acc[u][i] = 0.f;
+            u4v kf[2][GK];
+#pragma unroll
+            for (int j = 0; j < GK; ++j) kf[0][j] = k_operand(buf, j);
+#pragma unroll
+            for (int i = 0; i < NK; i += GK) {
+                if (i + GK < NK) {
+#pragma unroll
+                    for (int j = 0; j < GK; ++j) kf[(i / GK + 1) & 1][j] = k_operand(buf, i + GK + j);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < GK; ++j) {
+                    const int u = (i + j) / (STEPS * AP), ap = AP - 1 - (i + j) / STEPS % AP, b = (i + j) % STEPS;
+#pragma unroll
+                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) acc[u] = mfma_of<BF>(kf[(i / GK) & 1][j], qf[b][k], acc[u]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) s[i] = acc[i / VL][i % VL];
+        }
+        u4v vf[2][GV];
+#pragma unroll
+        for (int j = 0; j < GV; ++j) vf[0][j] = v_operand(buf, j);
+        __builtin_amdgcn_sched_barrier(0);
+        soften(t, f);
 #pragma unroll
         for (int kk = 0; kk < kKeys / KS; ++kk) {
             u4v pf[BP];
@@ -504,9 +532,9 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             constexpr int N = NO * AP;
 #pragma unroll
             for (int i = kk * N; i < kk * N + N; i += GV) {
-                if (i + GV < kKeys / KS * N) {
+                if (i + GV < NV) {
 #pragma unroll
-                    for (int j = 0; j < GV; ++j) vf[(i / GV + 1) & 1][j] = v_operand(i + GV + j);
+                    for (int j = 0; j < GV; ++j) vf[(i / GV + 1) & 1][j] = v_operand(buf, i + GV + j);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
