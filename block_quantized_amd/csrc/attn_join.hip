@@ -8,7 +8,9 @@ namespace {
 // Joins the splits of `each` rows and heads a workgroup, those that have more
 // than one (a batch of thousands of short sequences has few).  Its four
 // wavefronts take a row's splits in turn: a lane four values, so 256 / (D / 4)
-// splits at a time.
+// splits at a time.  A kernel of its own rather than the last workgroup's work:
+// 32 rows of 64 splits take 6.2 us, most of it the launch and a chain of three
+// loads; 2048 rows of 3 to 6 splits 6.8 us.
 template <int D, bool XB>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int each) {
     constexpr int LANES = D / 4, AT = 256 / LANES;  // lanes of a split, splits at a time
