@@ -19,7 +19,10 @@
 // in the cache is one page lookup, the same for its lanes.  The next tile's
 // loads are issued before a tile is multiplied.
 //
-// Exactness: bf16 queries take one product with 16-bit P.  fp32 queries and P
+// Exactness: bf16 queries take one product with P in 16 bits, the cache's kind
+// (so that the same MFMA takes both): fp16's 11 bits cost a bf16 result nothing,
+// bf16's 8 as much as the result's own rounding (0.0023 instead of 0.0017 of the
+// norm; a second part would add half of the products again).  fp32 queries and P
 // are split into two fp16 parts (three bf16 ones for a bf16 cache), and the
 // values of Q8_0 rows, d times a code, into two fp16 parts: three products of
 // parts instead of one.  Q8_0 values are staged times a power of two, the

@@ -458,3 +458,17 @@ def test_python_refuses_what_ctypes_would_cut():
         assert e.value.code == Q.QMM_ERR_UNSUPPORTED
     with pytest.raises(Q.QmmError):
         Q.rope_freqs(2 ** 32 + 64, 1e4)
+
+
+@pytest.mark.parametrize("cache", [R.Q8, R.F16, R.BF16])
+@pytest.mark.parametrize("xt", [R.F32, R.BF16])
+def test_long_walks_of_the_tile_kernels(cache, xt):
+    # more than 64 tiles of 64 keys in one part: page numbers are looked up for
+    # 64 tiles together; a bound on the length that is too low keeps the part whole
+    g = synth.rng(32)
+    b, c, kb, ks, vs = setup(g, [(3, 8300), (2, 4200)], 64, cache, 1, 64)
+    q = R.as_type(synth.normal_f32(g, (b.N, 2, 64)), xt)
+    for max_kv in (64, 0):
+        kb = Q.KVBatch(kb.q_start, kb.kv_len, kb.table, b.N, max_kv=max_kv)
+        run(b, c, kb, ks, vs, q, xt, 1, 64, 2)
+        run(b, c, kb, ks, vs, q, xt, 1, 64, 2, window=100, prefix=[5000, 4200])

@@ -149,3 +149,20 @@ def test_garbage_metadata_stays_in_bounds():
         Q.kv_append(c, kb, x, x, q=x, rope=Q.Rope(to_gpu(R.freqs64(64)), 0))
         torch.cuda.synchronize()
     assert torch.equal(c.k, guard)
+
+
+def test_rows_of_any_contents_are_the_quantizers():
+    # infinities, NaN, zeros of both signs, subnormals, blocks whose scale
+    # overflows or vanishes: byte for byte what the activation quantizer stores
+    g = synth.rng(9)
+    b = R.Batch(g, [(64, 64)], 64)
+    x = synth.normal_f32(g, (64, 2, 64)) * np.float32(10.0) ** g.integers(-44, 38, (64, 2, 1)).astype(np.float32)
+    odd = np.array([np.inf, -np.inf, np.nan, 0.0, -0.0, 1e-45, 3e38, -3e38], np.float32)
+    x[:8, 0, 5] = odd
+    x[8:16, 1, :32] = 0.0
+    x[8:16, 1, 40] = odd
+    c = make(g, R.Q8, 2, 64, b)
+    Q.kv_append(c, kv_batch(b), to_gpu(x), to_gpu(x))
+    want = to_cpu(Q.quantize_act(Q.QMM_Q8_0, to_gpu(x.reshape(64, 128)))).reshape(64, 2, 68)
+    for pool in (c.k, c.v):
+        assert_bytes_equal(to_cpu(pool), expect(b, want, R.Q8, 2, tuple(pool.shape)))
