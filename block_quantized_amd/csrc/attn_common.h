@@ -70,11 +70,11 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
                codes_f16(hi, 0x04030402u)};
 }
 
-// x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront
-// is below 0.35, as scores mostly are, the Taylor series to x^11 (the next term
-// is below 4e-9 x; COARSE, for bf16 results: to x^7, below 2e-6 x); elsewhere
-// 1 - 2 / (e^2x + 1), which loses bits to cancellation near 0, so that small
-// values keep the series.
+// x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront is below
+// 0.35, as scores mostly are, x times the polynomial in x^2 that is closest to
+// tanh(x) / x there: of degree 4, 4e-10 off relative to it (COARSE, for bf16
+// results: of degree 2, 3e-6); elsewhere 1 - 2 / (e^2x + 1), which loses bits to
+// cancellation near 0, so that small values keep the polynomial.
 template <bool COARSE, int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
     const float in = f / cap, out = cap * kLog2e;
@@ -88,14 +88,15 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float x2 = x[i] * x[i];
-        float p = -17.0f / 315.0f;
-        if constexpr (!COARSE) {
-            p = fmaf(-1382.0f / 155925.0f, x2, 62.0f / 2835.0f);
-            p = fmaf(p, x2, -17.0f / 315.0f);
+        float t;
+        if constexpr (COARSE) {
+            t = x[i] * fmaf(fmaf(0.123950313f, x2, -0.332909541f), x2, 0.999997131f);
+        } else {
+            float p = fmaf(0.0193613345f, x2, -0.0537063462f);
+            p = fmaf(p, x2, 0.133322014f);
+            p = fmaf(p, x2, -0.333333161f);
+            t = fmaf(p * x2, x[i], x[i]);
         }
-        p = fmaf(p, x2, 2.0f / 15.0f);
-        p = fmaf(p, x2, -1.0f / 3.0f);
-        float t = fmaf(p * x2, x[i], x[i]);
         if (large) {
             const float e = __builtin_amdgcn_exp2f(2.0f * kLog2e * fabsf(x[i]));
             const float u = copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), x[i]);
