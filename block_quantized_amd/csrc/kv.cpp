@@ -105,27 +105,53 @@ int64_t key_bound(const qmm_kv_cache* c, const qmm_kv_batch* b) {
     return b->max_kv > 0 && b->max_kv < room ? b->max_kv : room;
 }
 
-// Tile kernels multiply 128 rows at a time and split kernels 16, but a tile
-// takes longer to begin and end: they win from 48 rows a sequence on (tokens x
-// query heads of a key-value head; 8 sequences of 1940 keys, 8 heads, Q8_0 and
-// fp32: 31 against 36 us at 32 rows, 48 against 47 at 64, 82 against 58 at
-// 128), and with few keys from as many as make some 10000 products of 16 rows
-// and 32 keys (one sequence: 31 against 36 us at 256 rows, 45 against 40 at 384).
-int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, int n_q) {
-    const int64_t rows = up_div(b->n_tokens * (n_q / c->n_kv), b->n_seqs);
-    return rows >= 48 && b->n_seqs * up_div(rows, 16) * c->n_kv * up_div(key_bound(c, b), 32) >= 10000 ? 2 : 1;
+// Tokens (log2) of a row tile of `rows` rows for `chunk` query heads: what
+// fits, but no more than a sequence has.
+int tile_tokens(int rows, int chunk, int64_t each) {
+    int shift = 0;
+    while ((2 << shift) * chunk <= rows && (1 << shift) < each) ++shift;
+    return shift;
+}
+
+// Split kernels spread 16 rows' products with 32 keys over the whole chip and
+// join them; tile kernels take 128 rows through tiles of 64 keys, one after
+// another.  So the former's time is some 12 us (27 for heads above 128, whose
+// waves' parts fill LDS; 6 less where nothing is joined) and 1 us for 1000 such
+// products of 64 values, the latter's some 9 us and 3 us a step, as many steps as
+// a row tile sees tiles of keys, times the rounds of 512 workgroups; or, their
+// keys split (128 row tiles at most), 22 us and 9.5 for each 512 steps.  Split against tile kernels, us: 1588 tokens, 14 heads on 2
+// of 64, fp32: 45, 56; 3 x 1078 of the same, bf16 over Q8_0: 71, 64; 2 x 892, 32
+// on 8 of 128: 90, 51; 397 behind 237, 32 heads of 128 each its own, fp32: 35,
+// 47; 314, 16 on 8 of 256, fp32: 37, 29; 462, 14 on 2 of 64: 22, 39; with a
+// window of 97, 3 x 1116: 36, 20; 328 behind 409, 32 on 8 of 128, fp32: 34, 48; 85
+// of 32 on 8 of 64: 8, 11.  Over 160 sizes drawn at random the choice costs 1.4%
+// (geometric mean) against the better one of each.  Below 48 rows a sequence most
+// of a tile is idle.
+int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
+    const int G = n_q / c->n_kv;
+    const int64_t each = up_div(b->n_tokens, b->n_seqs), rows = up_div(b->n_tokens * G, b->n_seqs);
+    if (rows < 48) return 1;
+    const int chunk = G < kTileRows ? G : kTileRows, shift = tile_tokens(kTileRows, chunk, each);
+    const double keys = (double)key_bound(c, b), seen = o->window > 0 && !o->prefix ? o->window : keys;
+    const double mean = fmin(fmax(keys - 0.5 * each, 1.0), seen);  // of a row
+    const double most = fmin(keys, seen + (1 << shift));           // of a row tile
+    const double split = (c->head_dim > 128 ? 27.0 : 12.0) - (fmin(keys, seen + each) > 128 ? 0.0 : 6.0) +
+                         1e-3 * b->n_seqs * up_div(rows, 16) * c->n_kv * (mean / 32) * (c->head_dim / 64.0);
+    const double groups = (double)(up_div(each, int64_t(1) << shift) * b->n_seqs) * c->n_kv * up_div(G, chunk);
+    const double steps = fmax(most / 64, 1.0);
+    const double tile = groups <= 128 && most > 128 ? 22.0 + 9.5 * steps * groups / 512
+                                                    : 9.0 + 3.0 * steps * fmax(groups / 512, 1.0);
+    return tile < split ? 2 : 1;
 }
 
 Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
     Plan p = {};
     const int G = n_q / c->n_kv;
-    p.algo = o->algo ? o->algo : choose(c, b, n_q);
+    p.algo = o->algo ? o->algo : choose(c, b, o, n_q);
     const int rows = p.algo == 2 ? kTileRows : kSplitRows;
     p.chunk = G < rows ? G : rows;
     p.chunks = (int)up_div(G, p.chunk);
-    // tokens of a row tile: what fits, but no more than a sequence has
-    const int64_t each = up_div(b->n_tokens, b->n_seqs);
-    while ((2 << p.shift) * p.chunk <= rows && (1 << p.shift) < each) ++p.shift;
+    p.shift = tile_tokens(rows, p.chunk, up_div(b->n_tokens, b->n_seqs));
     int64_t tiles = (b->n_tokens >> p.shift) + b->n_seqs;  // row tiles at most
     if (tiles > b->n_tokens) tiles = b->n_tokens;
     int64_t keys = key_bound(c, b);
@@ -136,13 +162,15 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     // leaves each below 2048 keys, among fewer, at least 512, two a CU (one of
     // 131k keys, 8 heads: 76 us with 512, 88 with 2048).  A part keeps 128 keys, a
     // tile a wave (one sequence of 1940: 14 us; with 256 keys 16, with 512 22).
-    // Prompts are split only where their row tiles are fewer than 512.
+    // Tile kernels split only what makes four parts and more of a row tile: fewer
+    // cost in writing and joining what they save (us with two, without: 309 tokens
+    // twice, 32 heads, 30 and 18; 602 tokens, a window of 17: 35 and 21).
     p.least = 4;
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
     int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
     s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
     if (s > most) s = most;
-    p.splits = keys > 32 * p.least && (p.algo == 1 || s > tiles) ? (int)s : 0;
+    p.splits = keys > 32 * p.least && (p.algo == 1 || s >= 4 * tiles) ? (int)s : 0;
     p.items = tiles + p.splits;
     p.slots = p.chunk << p.shift;
     p.parts = p.splits ? p.items * heads * p.slots : 0;

@@ -155,7 +155,8 @@ size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const
 
 /* The kernel family that algo 0 takes for these sizes: 1 = split kernels
  * (few rows a sequence; bound by reading the cache), 2 = tile kernels; 0 for
- * sizes that qmm_attn rejects. */
+ * sizes that qmm_attn rejects.  With a window fewer keys count, and the choice
+ * may be another. */
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q);
 
 #ifdef __cplusplus

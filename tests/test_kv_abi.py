@@ -129,6 +129,10 @@ def test_choice():
     assert Q.qmm_attn_choice(cache(), batch(), Q.QMM_F32, 3) == 0
     assert Q.qmm_attn_choice(cache(), batch(), Q.QMM_F16, 4) == 0
     assert Q.qmm_attn_choice(cache(page_size=15), batch(), Q.QMM_F32, 4) == 0
+    # single tokens and short questions take the split kernels, prompts the tile kernels
+    c = cache(n_kv=8, page_size=64)
+    for n_seqs, n_tokens, width, want in ((64, 64, 256, 1), (1, 61, 32, 1), (1, 2048, 32, 2), (4, 8000, 35, 2)):
+        assert Q.qmm_attn_choice(c, batch(n_seqs=n_seqs, n_tokens=n_tokens, table_width=width), Q.QMM_F32, 32) == want
 
 
 def test_grids_of_too_many_workgroups():
