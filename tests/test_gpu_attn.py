@@ -472,3 +472,16 @@ def test_long_walks_of_the_tile_kernels(cache, xt):
         kb = Q.KVBatch(kb.q_start, kb.kv_len, kb.table, b.N, max_kv=max_kv)
         run(b, c, kb, ks, vs, q, xt, 1, 64, 2)
         run(b, c, kb, ks, vs, q, xt, 1, 64, 2, window=100, prefix=[5000, 4200])
+
+
+@pytest.mark.parametrize("xt", [R.F32, R.BF16])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_joins_of_many_rows(xt, dim):
+    # from 2048 rows and heads on the join gives each wavefront rows of its own
+    g = synth.rng(33)
+    seqs = [(1, 1100)] + [(1, 1 + (37 * i) % 50) for i in range(64)] + [(0, 9), (3, 600)]
+    b, c, kb, ks, vs = setup(g, seqs, 16, R.F16, 1, dim)
+    q = R.as_type(synth.normal_f32(g, (b.N, 32, dim)), xt)
+    assert b.N * 32 >= 2048 and Q.qmm_attn_work(c.c, kb.c, Q.qmm_attn_opts(0.1, 0.0, 0, 1, None, None), Q.QMM_F32, 32) > 0
+    run(b, c, kb, ks, vs, q, xt, 1, dim, 1)
+    run(b, c, kb, ks, vs, q, xt, 1, dim, 1, window=300)
