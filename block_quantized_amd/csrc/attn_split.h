@@ -24,8 +24,8 @@
 // P is 2^8 p, and P d is kept below 2^15 by a power of two per wave: the fp16
 // parts lose nothing to subnormals.
 //
-// The running maximum of a row is raised only when a score is above it by
-// more than 2^7: p may reach 2^7, which costs fp32 sums nothing and saves the
+// The running maximum of a row is raised only when a score (times log2 e) is
+// above it by more than 7: p may reach 2^7, which costs fp32 sums nothing and saves the
 // cross-lane maximum and the rescaling for almost every tile.
 //
 // Bound: reading the cache.  fp32 queries, 32 heads, of 128 values, on 8 of the

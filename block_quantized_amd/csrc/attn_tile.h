@@ -433,7 +433,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     };
     float s[R];
     // From the products of tile t to scores (f s, times log2 e), masked; raises
-    // the running maximum where they pass it by 2^7.
+    // the running maximum where they pass it by 7.
     auto soften = [&](int t, float& f) {
         const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
         bool page[4];  // of each 16 keys

@@ -7,8 +7,8 @@
 // unit is built with -ffp-contract=off like that one.
 //
 // Bound: reading the rows and writing them once.  Five prompts, 6777 tokens in
-// all (fp32, 32 query and 8 key-value heads of 128, Q8_0 cache; 292 MB): 61-68
-// us, 4.3-4.8 TB/s, of the 5.1 that a large copy reaches.  With the sines
+// all (fp32, 32 query and 8 key-value heads of 128, Q8_0 cache; 292 MB): 61-70
+// us, 4.2-4.8 TB/s, of the 5.1 that a large copy reaches.  With the sines
 // computed by every head and several tokens a workgroup it took some 30 us more.
 // 48 tokens take 5.1 us, one 4.0: a chain of loads (q_start, table, row).
 #include "kv_internal.h"
