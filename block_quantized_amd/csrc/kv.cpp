@@ -144,7 +144,7 @@ int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o,
     return tile < split ? 2 : 1;
 }
 
-Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
+Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int xtype, int n_q) {
     Plan p = {};
     const int G = n_q / c->n_kv;
     p.algo = o->algo ? o->algo : choose(c, b, o, n_q);
@@ -164,13 +164,17 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     // tile a wave (one sequence of 1940: 14 us; with 256 keys 16, with 512 22).
     // Tile kernels split only what makes four parts and more of a row tile: fewer
     // cost in writing and joining what they save (us with two, without: 309 tokens
-    // twice, 32 heads, 30 and 18; 602 tokens, a window of 17: 35 and 21).
+    // twice, 32 heads, 30 and 18; 602 tokens, a window of 17: 35 and 21).  Where a
+    // step is long, that is for wide heads over Q8_0 rows and with fp32 queries over
+    // bf16 rows, two parts pay (2048 tokens, 16 heads on 4 of 256: Q8_0 168 and 224,
+    // with bf16 queries 111 and 139; bf16 rows 148 and 180; but fp16 rows 118, 112).
     p.least = 4;
+    const bool heavy = c->head_dim > 128 && (c->type == QMM_Q8_0 || (c->type == QMM_BF16 && xtype == QMM_F32));
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
     int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
     s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
     if (s > most) s = most;
-    p.splits = keys > 32 * p.least && (p.algo == 1 || s >= 4 * tiles) ? (int)s : 0;
+    p.splits = keys > 32 * p.least && (p.algo == 1 || s >= 4 * tiles || (heavy && s > tiles)) ? (int)s : 0;
     p.items = tiles + p.splits;
     p.slots = p.chunk << p.shift;
     p.parts = p.splits ? p.items * heads * p.slots : 0;
@@ -276,14 +280,14 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q)) return 0;
     const qmm_attn_opts none = {};
-    const Plan p = plan(cache, batch, &none, n_q);
+    const Plan p = plan(cache, batch, &none, xtype, n_q);
     return fits(cache, batch, n_q, p) ? p.algo : 0;
 }
 
 size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
                      int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
-    const Plan p = plan(cache, batch, opts, n_q);
+    const Plan p = plan(cache, batch, opts, xtype, n_q);
     return fits(cache, batch, n_q, p) ? work_bytes_of(cache, batch, n_q, p) : 0;
 }
 
@@ -293,7 +297,7 @@ int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_att
     if ((rc = check_xtype(xtype)) || (rc = check_cache(cache)) || (rc = check_batch(cache, batch))) return rc;
     if ((rc = check_attn_sizes(cache, batch, xtype, n_q)) || (rc = check_opts(opts))) return rc;
     if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, cache->head_dim)) || (rc = check_ptr(out))) return rc;
-    const Plan p = plan(cache, batch, opts, n_q);
+    const Plan p = plan(cache, batch, opts, xtype, n_q);
     if (!fits(cache, batch, n_q, p)) return QMM_ERR_SHAPE;
     const size_t need = work_bytes_of(cache, batch, n_q, p);
     if (need) {
