@@ -160,8 +160,12 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     // that the last of them end together (64 conversations of 8k to 16k keys: 397 us
     // with 512 workgroups, 362 with 1024, 338 with 2048, 340 with 2560); where that
     // leaves each below 2048 keys, among fewer, at least 512, two a CU (one of
-    // 131k keys, 8 heads: 76 us with 512, 88 with 2048).  A part keeps 128 keys, a
-    // tile a wave (one sequence of 1940: 14 us; with 256 keys 16, with 512 22).
+    // 131k keys, 8 heads: 76 us with 512, 88 with 2048), less one a row tile, which
+    // may add a part that is not full, so that all run at once (three a CU, two for
+    // heads above 128; us without, with: 10 sequences, 3341 keys, 8 heads of 256 in
+    // bf16: 89, 67; 7 of 9000 in Q8_0: 77, 59; 13 of 1400, 32 of 128: 57, 49).  A
+    // part keeps 128 keys, a tile a wave (one sequence of 1940: 14 us; with 256 keys
+    // 16, with 512 22).
     // Tile kernels split only what makes four parts and more of a row tile: fewer
     // cost in writing and joining what they save (us with two, without: 309 tokens
     // twice, 32 heads, 30 and 18; 602 tokens, a window of 17: 35 and 21).  Where a
@@ -172,7 +176,9 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     const bool heavy = c->head_dim > 128 && (c->type == QMM_Q8_0 || (c->type == QMM_BF16 && xtype == QMM_F32));
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
     int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
-    s = up_div(s < 512 || p.algo == 2 ? 512 : s > 2048 ? 2048 : s, heads);
+    const int64_t slots = c->head_dim > 128 ? 512 : 768, rest = slots - tiles * heads;
+    const int64_t low = p.algo == 2 || rest < 256 || rest > 512 ? 512 : rest;
+    s = up_div(s < low || p.algo == 2 ? low : s > 2048 ? 2048 : s, heads);
     if (s > most) s = most;
     p.splits = keys > 32 * p.least && (p.algo == 1 || s >= 4 * tiles || (heavy && s > tiles)) ? (int)s : 0;
     p.items = tiles + p.splits;
