@@ -72,10 +72,10 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
 
 // x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront is below
 // 0.35, as scores mostly are, x times the polynomial in x^2 that is closest to
-// tanh(x) / x there: of degree 4, 4e-10 off relative to it (COARSE, for bf16
-// results: of degree 2, 3e-6); elsewhere 1 - 2 / (e^2x + 1), which loses bits to
-// cancellation near 0, so that small values keep the polynomial.
-template <bool COARSE, int N>
+// tanh(x) / x there: of degree 4, 9e-10 off relative to it; elsewhere
+// 1 - 2 / (e^2x + 1), which loses bits to cancellation near 0, so that small
+// values keep the polynomial.
+template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
     const float in = f / cap, out = cap * kLog2e;
     float big = 0.f;
@@ -88,15 +88,10 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float x2 = x[i] * x[i];
-        float t;
-        if constexpr (COARSE) {
-            t = x[i] * fmaf(fmaf(0.123950313f, x2, -0.332909541f), x2, 0.999997131f);
-        } else {
-            float p = fmaf(0.0193613345f, x2, -0.0537063462f);
-            p = fmaf(p, x2, 0.133322014f);
-            p = fmaf(p, x2, -0.333333161f);
-            t = fmaf(p * x2, x[i], x[i]);
-        }
+        float p = fmaf(0.0193613345f, x2, -0.0537063462f);
+        p = fmaf(p, x2, 0.133322014f);
+        p = fmaf(p, x2, -0.333333161f);
+        float t = fmaf(p * x2, x[i], x[i]);
         if (large) {
             const float e = __builtin_amdgcn_exp2f(2.0f * kLog2e * fabsf(x[i]));
             const float u = copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), x[i]);

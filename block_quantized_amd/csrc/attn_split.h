@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = kept(i >> 2, kb + 16 * (i >> 2) + 4 * g + (i & 3)) ? sc[i] : 0.f;
         }
-        if (a.softcap > 0.f) cap_scores<false>(sc, 1.0f, a.softcap);
+        if (a.softcap > 0.f) cap_scores(sc, 1.0f, a.softcap);
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -19,13 +19,16 @@
 // in the cache is one page lookup, the same for its lanes.  The next tile's
 // loads are issued before a tile is multiplied.
 //
-// Exactness: bf16 queries take one product with P in 16 bits, the cache's kind
-// (so that the same MFMA takes both): fp16's 11 bits cost a bf16 result nothing,
-// bf16's 8 as much as the result's own rounding (0.0023 instead of 0.0017 of the
-// norm; a second part would add half of the products again).  fp32 queries and P
-// are split into two fp16 parts (three bf16 ones for a bf16 cache), and the
-// values of Q8_0 rows, d times a code, into two fp16 parts: three products of
-// parts instead of one.  Q8_0 values are staged times a power of two, the
+// Exactness: bf16 queries are operands as they are, and P is split into two parts
+// of the cache's kind, which hold 22 bits (fp16) or 16: a bf16 result is the fp32
+// one rounded, as the split kernels' is, so that it does not depend on the sizes
+// that choose between them.  (With one part, 8 or 11 bits, 8191 tokens took 610 us
+// instead of 790 over bf16 rows and 630 instead of 830 over fp16 rows, but the
+// former's error was 0.0023 of the norm instead of 0.0017, and a tenth of the
+// latter's results were neighbours of the right ones.)  fp32 queries and P are split
+// into two fp16 parts (three bf16 ones for a bf16 cache), and the values of Q8_0
+// rows, d times a code, into two fp16 parts, which hold them exactly: three products
+// of parts instead of one, and with bf16 queries two for scores and three for P V.  Q8_0 values are staged times a power of two, the
 // same for all keys of a tile (and one for its values), that keeps the largest
 // below 2^15.
 //
@@ -85,15 +88,17 @@ struct Staged {
 
 // The largest group of operands, up to `most`, that n of them divide into.
 constexpr int group_of(int n, int most) { return n % most ? group_of(n, most - 1) : most; }
-// Parts of Q and P, and rows of a wave.
+// Parts of Q and of P, and rows of a wave.
 constexpr int q_parts(int ct, bool xb) { return xb ? 1 : ct == QMM_BF16 ? 3 : 2; }
+constexpr int p_parts(int ct, bool xb) { return xb ? 2 : q_parts(ct, xb); }
 constexpr int wave_rows(int ct, int nb, bool xb) { return nb > 4 || q_parts(ct, xb) == 3 ? 16 : 32; }
 
 template <int CT, int NB, bool XB>
 __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void attn_tile_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
-    constexpr int AP = Q8 && !XB ? 2 : 1, BP = q_parts(CT, XB);  // parts of K and V, of Q and P
+    constexpr int AP = Q8 ? 2 : 1;                               // parts of K and V
+    constexpr int QP = q_parts(CT, XB), PP = p_parts(CT, XB);    // of Q, of P
     constexpr int R = wave_rows(CT, NB, XB), W = kTileRows / R;  // rows of a wave, waves
     constexpr int GROUPS = 64 / R, KS = 8 * GROUPS;              // lanes of a row, values (or keys) of an MFMA's step
     constexpr int KPW = kKeys / W;                               // keys that a wave stages
@@ -139,7 +144,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     auto k_at = [&](int key, int col) { return key * KROW + 16 * (R == 32 || NB % 2 ? col : col ^ ((key >> 2) & 4)); };
 
     // ---- the queries, as B operands: lane (r, h) holds the values 8h..8h+7 of each step
-    u4v qf[D / KS][BP];
+    u4v qf[D / KS][QP];
     float qs;
     {
         const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D + 8 * h;
@@ -181,10 +186,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t part[BP];
-                split_pair<BF, BP>(x[2 * i] * up, x[2 * i + 1] * up, part);
+                uint32_t part[QP];
+                split_pair<BF, QP>(x[2 * i] * up, x[2 * i + 1] * up, part);
 #pragma unroll
-                for (int k = 0; k < BP; ++k) qf[b][k][i] = part[k];
+                for (int k = 0; k < QP; ++k) qf[b][k][i] = part[k];
             }
         }
     }
@@ -440,7 +445,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 #pragma unroll
         for (int i = 0; i < 4; ++i) page[i] = s_page[t & 1][W / 4 * i] != 0;
         if (capped) {
-            cap_scores<XB>(s, f, a.softcap);
+            cap_scores(s, f, a.softcap);
             f = 1.0f;
         }
         if (a.slopes) {
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         if (idle || !((kb < at.pre) || (kb <= p_last && kb < at.len && kb + kKeys - 1 >= low_first))) continue;
         // Operands come from LDS some at a time, the next ones while these are
         // multiplied: left to itself the compiler waits for each before its use.
-        constexpr int GK = group_of(NK, BP > 1 ? 2 : 4), GV = group_of(NO * AP, BP > 1 ? 2 : 4);
+        constexpr int GK = group_of(NK, QP > 1 ? 2 : 4), GV = group_of(NO * AP, QP > 1 ? 2 : 4);
         {
             accv acc[SUBS];
 #pragma unroll
@@ -520,7 +525,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 for (int j = 0; j < GK; ++j) {
                     const int u = (i + j) / (STEPS * AP), ap = AP - 1 - (i + j) / STEPS % AP, b = (i + j) % STEPS;
 #pragma unroll
-                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) acc[u] = mfma_of<BF>(kf[(i / GK) & 1][j], qf[b][k], acc[u]);
+                    for (int k = (ap ? 0 : QP - 1); k >= 0; --k) acc[u] = mfma_of<BF>(kf[(i / GK) & 1][j], qf[b][k], acc[u]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -534,16 +539,16 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         soften(t, f);
 #pragma unroll
         for (int kk = 0; kk < kKeys / KS; ++kk) {
-            u4v pf[BP];
+            u4v pf[PP];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float x = __builtin_amdgcn_exp2f(fmaf(s[8 * kk + 2 * i], f, -mref));
                 const float y = __builtin_amdgcn_exp2f(fmaf(s[8 * kk + 2 * i + 1], f, -mref));
                 l += x + y;
-                uint32_t part[BP];
-                split_pair<BF, BP>(x, y, part);
+                uint32_t part[PP];
+                split_pair<BF, PP>(x, y, part);
 #pragma unroll
-                for (int k = 0; k < BP; ++k) pf[k][i] = part[k];
+                for (int k = 0; k < PP; ++k) pf[k][i] = part[k];
             }
             constexpr int N = NO * AP;
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 for (int j = 0; j < GV; ++j) {
                     const int c = (i + j) / AP % NO, ap = AP - 1 - (i + j) % AP;
 #pragma unroll
-                    for (int k = (ap ? 0 : BP - 1); k >= 0; --k) o[c] = mfma_of<BF>(vf[(i / GV) & 1][j], pf[k], o[c]);
+                    for (int k = (ap ? 0 : PP - 1); k >= 0; --k) o[c] = mfma_of<BF>(vf[(i / GV) & 1][j], pf[k], o[c]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }

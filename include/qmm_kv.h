@@ -141,7 +141,8 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
  *   work  : device, qmm_attn_work(...) bytes for the same arguments, 16-byte
  *           aligned; may be NULL when that is 0.  Calls that may run at the
  *           same time need one each; contents need not be kept.
- * Fp32 results are as exact as a product in fp32.  What lies in the cache at
+ * Fp32 results are as exact as a product in fp32, bf16 results are these
+ * rounded once, whichever kernels compute them.  What lies in the cache at
  * places that no row of the call sees has no effect, infinities and NaN
  * included; visible keys and values have to be finite.  Batches whose grids
  * would pass 2^32 work-items are refused (QMM_ERR_SHAPE). */
