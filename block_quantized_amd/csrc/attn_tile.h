@@ -167,10 +167,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         int ex = 0;
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);
-        // the sign of the scale goes to the queries, and no scale is 0: masked scores stay -inf times it
+        // the sign of the scale goes to the queries
         constexpr int TOP = BF ? 0 : 14;  // (bf16 parts have fp32's range)
         const float up = copysignf(ldexpf(1.0f, TOP - ex), a.scale);
-        qs = fmaxf(ldexpf(1.0f, ex - TOP) * fabsf(a.scale), 0x1p-120f);
+        qs = ldexpf(1.0f, ex - TOP) * fabsf(a.scale);
 #pragma unroll
         for (int b = 0; b < D / KS; ++b) {
             float x[8];
@@ -496,6 +496,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             store_k(1.0f, buf);
             store_v(1.0f, buf);
         }
+        f = fmaxf(f, 0x1p-120f);  // never 0: masked scores stay -inf times it
         __syncthreads();
         if (t + 1 < t1) begin(t + 1);
 
