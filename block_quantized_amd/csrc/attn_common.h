@@ -77,7 +77,7 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
 // values keep the polynomial.
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float f, float cap) {
-    const float in = f / cap, out = cap * kLog2e;
+    const float in = fminf(f / cap, 0x1p127f), out = cap * kLog2e;  // finite: a score of 0 stays 0
     float big = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
