@@ -55,6 +55,15 @@ __device__ __forceinline__ f4v mfma16(u4v a, u4v b, f4v c) {
                                                       0, 0, 0);
 }
 
+// Two int8 codes, bytes I and J of w, as bf16 (exactly: they have 7 bits).  (The
+// empty asm hides how w was put together, else bytes are shifted out one by one.)
+template <int I, int J>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+    asm("" : "+v"(w));
+    const float x = (float)(int8_t)(w >> (8 * I)), y = (float)(int8_t)(w >> (8 * J));
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y), __builtin_bit_cast(uint32_t, x), 0x07060302u);
+}
+
 // Two int8 codes, bytes `sel` of x ^ 0x80808080 (so code + 128), as fp16:
 // 0x6400 | u is 1024 + u, and 1152 less is the code, exactly.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t biased, uint32_t sel) {
@@ -69,6 +78,15 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
     return u4v{codes_f16(lo, 0x04010400u), codes_f16(lo, 0x04030402u), codes_f16(hi, 0x04010400u),
                codes_f16(hi, 0x04030402u)};
 }
+
+// The running maximum of a row is raised when a score (times log2 e) passes it by
+// this: weights reach 2^kSlack, which spares the cross-lane maximum and the
+// rescaling for almost every tile.
+constexpr float kSlack = 1.0f;
+// Weights carry a factor of 2^p_top: fp16 parts then reach down to 2^-39 of the
+// largest weight; bf16 parts have fp32's range.
+template <bool BF>
+__device__ __forceinline__ constexpr float p_top() { return BF ? 0.0f : 14.0f; }
 
 // x = cap * tanh(f x / cap) * log2 e.  Where every |f x / cap| of the wavefront is below
 // 0.35, as scores mostly are, x times the polynomial in x^2 that is closest to

@@ -17,16 +17,16 @@
 // lane (m, g) ends with the eight consecutive values 8g..8g+7 of each block.
 //
 // Exactness: the cache's values enter the MFMAs as they are (fp16 and bf16
-// rows; Q8_0 codes as fp16 integers, their block scales applied to the fp32
-// block scores, and to P before it is rounded).  Queries and P are split into
-// 16-bit parts that hold 22 bits (two fp16) or 24 (three bf16).  Queries are
-// scaled by a power of two per row so that their largest value is about 2^14,
-// P is 2^8 p, and P d is kept below 2^15 by a power of two per wave: the fp16
-// parts lose nothing to subnormals.
-//
-// The running maximum of a row is raised only when a score (times log2 e) is
-// above it by more than 7: p may reach 2^7, which costs fp32 sums nothing and saves the
-// cross-lane maximum and the rescaling for almost every tile.
+// rows; Q8_0 codes as fp16 integers for K, as bf16 ones for V, their block scales
+// applied to the fp32 block scores, and to P before it is split).  Queries and P
+// are split into 16-bit parts that hold 22 bits (two of fp16) or 24 (three of
+// bf16).  bf16 parts have fp32's range, and so take the P d of Q8_0 rows, whose
+// sizes go by the cache.  (In two fp16 parts, kept below 2^15 by one power of two a
+// wave, they took 325 us instead of 340 for 64 of 8k to 16k keys, but a block whose
+// d was 2^20 below another's kept 12 bits.)  Where parts are fp16, queries are
+// scaled by a power of two per row so that their largest value is about 2^14, and P
+// is 2^14 p: what is more than 2^16 below a row's largest is held to 2^-38 of that,
+// the parts' smallest step.
 //
 // Bound: reading the cache.  fp32 queries, 32 heads, of 128 values, on 8 of the
 // cache's: one sequence of 131k keys in Q8_0 (285 MB) 61 us, 4.7 TB/s; 64 of
@@ -46,9 +46,6 @@ namespace {
 
 constexpr int kWaves = 4;
 
-template <int CT>
-__device__ __forceinline__ constexpr int parts_of() { return CT == QMM_BF16 ? 3 : 2; }
-
 __device__ __forceinline__ uint32_t ld16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
 // Q8_0: LDS bytes of a wave's 32 keys or values, blocks and their scales.
@@ -57,13 +54,15 @@ constexpr int kStage = 32 * 34 * NB + 64 * NB;
 
 template <int CT, int NB, bool XB>
 __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
-    constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D), PARTS = parts_of<CT>();
-    constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
+    constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
+    // the parts of P, and those of Q, with the MFMAs that take them
+    constexpr bool BF = CT != QMM_F16, Q8 = CT == QMM_Q8_0, QBF = CT == QMM_BF16;
+    constexpr int PP = BF ? 3 : 2, QP = QBF ? 3 : 2;
     // LDS: the queries and the waves' staging regions, then the waves' parts
-    constexpr int PARTS_BYTES = kWaves * 16 * (D + 4) * 4, Q_BYTES = NB * PARTS * 64 * 16;
+    constexpr int PARTS_BYTES = kWaves * 16 * (D + 4) * 4, Q_BYTES = NB * QP * 64 * 16;
     constexpr int USED_BYTES = Q_BYTES + (Q8 ? kWaves * kStage<NB> : 0);
     __shared__ __attribute__((aligned(16))) uint8_t smem[PARTS_BYTES > USED_BYTES ? PARTS_BYTES : USED_BYTES];
-    u4v(*s_q)[PARTS][64] = reinterpret_cast<u4v(*)[PARTS][64]>(smem);
+    u4v(*s_q)[QP][64] = reinterpret_cast<u4v(*)[QP][64]>(smem);
     const int groups = a.c.n_kv * a.chunks, item = (int)(blockIdx.x / groups), hb = blockIdx.x % groups;
     Work w;
     if (!find_work(a, item, w)) return;
@@ -146,22 +145,22 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         int ex = 0;
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);  // an all-zero row: any finite scale does
-        constexpr int TOP = BF ? 0 : 14;  // (bf16 parts have fp32's range)
+        constexpr int TOP = QBF ? 0 : 14;  // (bf16 parts have fp32's range)
         const float up = ldexpf(1.0f, TOP - ex);
         qs = ldexpf(1.0f, ex - TOP) * a.scale;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             if ((b & 3) != wave) continue;
-            u4v q[PARTS];
+            u4v q[QP];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t part[PARTS];
-                split_pair<BF, PARTS>(x[b][2 * i] * up, x[b][2 * i + 1] * up, part);
+                uint32_t part[QP];
+                split_pair<QBF, QP>(x[b][2 * i] * up, x[b][2 * i + 1] * up, part);
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) q[k][i] = part[k];
+                for (int k = 0; k < QP; ++k) q[k][i] = part[k];
             }
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) s_q[b][k][lane] = q[k];
+            for (int k = 0; k < QP; ++k) s_q[b][k][lane] = q[k];
         }
     }
     __syncthreads();
@@ -173,8 +172,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     f4v o[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) o[b][0] = o[b][1] = f4v{0.f, 0.f, 0.f, 0.f};
-    float mx = -INFINITY, mref = 0.f, l = 0.f;  // maximum, the same less 8 or 0, the lane's part of the sum
-    float vlim = 0x1p-30f, vinv = 0x1p30f;      // Q8_0: a power of two that no |d| seen is above, and 1 / it
+    float mx = -INFINITY, mref = 0.f, l = 0.f;  // maximum, the same less p_top or 0, the lane's part of the sum
 
     // whether any row sees the key in half u of the tile: others may hold anything, and count as 0
     auto kept = [&](int u, int key) {
@@ -204,13 +202,13 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
             }
         }
         float big = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-        if (__any(big > mx + 7.0f)) {
+        if (__any(big > mx + kSlack)) {
             big = fmaxf(big, __shfl_xor(big, 16));
             big = fmaxf(big, __shfl_xor(big, 32));
             const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
             const float down = __builtin_amdgcn_exp2f(mx - ref);  // 0 from -inf
             mx = top;
-            mref = ref - 8.0f;  // p carries a factor of 2^8
+            mref = ref - p_top<BF>();
             l *= down;
 #pragma unroll
             for (int b = 0; b < NB; ++b) o[b][0] *= down, o[b][1] *= down;
@@ -283,9 +281,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                 f4v sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    u4v qf[PARTS];
+                    u4v qf[QP];
 #pragma unroll
-                    for (int k = 0; k < PARTS; ++k) qf[k] = s_q[b][k][lane];
+                    for (int k = 0; k < QP; ++k) qf[k] = s_q[b][k][lane];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         // Codes begin 2 bytes behind a multiple of 4 in every
@@ -305,7 +303,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                         const u4v kf = codes8_f16(w);
                         f4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int k = PARTS - 1; k >= 0; --k) acc = mfma16<BF>(kf, qf[k], acc);
+                        for (int k = QP - 1; k >= 0; --k) acc = mfma16<QBF>(kf, qf[k], acc);
                         const uint2 d = *reinterpret_cast<const uint2*>(tab + 64 * b + 32 * u + 8 * g);
                         sum[u][0] = fmaf(acc[0], h2f(d.x), sum[u][0]);
                         sum[u][1] = fmaf(acc[1], h2f(d.x >> 16), sum[u][1]);
@@ -320,31 +318,17 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
             // ---- O^T += V^T (P d)^T
             settle();
             stage();
-            float dmax = 0.f;
+            if (!whole) {
 #pragma unroll
-            for (int j = 0; j < DL; ++j)
-                if (NB % 2 == 0 || dblk + 2 * j < NB) {
-                    if (!whole) din[j] = kept(dkey >> 4, kb + dkey) ? din[j] : 0;
-                    dmax = fmaxf(dmax, fabsf(h2f(din[j])));
-                }
+                for (int j = 0; j < DL; ++j)
+                    if (NB % 2 == 0 || dblk + 2 * j < NB) din[j] = kept(dkey >> 4, kb + dkey) ? din[j] : 0;
+            }
             scales();
             place(t + kWaves);  // behind the last tile, row 0 of the cache
             load(a.c.k);
-            if (__any(dmax > vlim)) {
-#pragma unroll
-                for (int k = 1; k < 64; k <<= 1) dmax = fmaxf(dmax, __shfl_xor(dmax, k));
-                int ex;
-                frexpf(fminf(dmax, 65504.0f), &ex);
-                const float lim = ldexpf(1.0f, ex), down = vlim / lim;
-                vlim = lim, vinv = 1.0f / lim;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][0] *= down, o[b][1] *= down;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc[i] *= vinv;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                u4v pf[PARTS], vf[2];
+                u4v pf[PP], vf[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint2 d = *reinterpret_cast<const uint2*>(tab + 64 * b + 32 * u + 8 * g);
@@ -352,19 +336,19 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t dd = i ? d.y : d.x;
-                        uint32_t part[PARTS];
-                        split_pair<BF, PARTS>(sc[4 * u + 2 * i] * h2f(dd), sc[4 * u + 2 * i + 1] * h2f(dd >> 16), part);
+                        uint32_t part[PP];
+                        split_pair<BF, PP>(sc[4 * u + 2 * i] * h2f(dd), sc[4 * u + 2 * i + 1] * h2f(dd >> 16), part);
 #pragma unroll
-                        for (int k = 0; k < PARTS; ++k) pf[k][2 * u + i] = part[k];
-                        const uint32_t w = (ld16(v + 2 * i * RB) | ld16(v + (2 * i + 1) * RB) << 16) ^ 0x80808080u;
-                        vf[0][2 * u + i] = codes_f16(w, 0x04020400u);
-                        vf[1][2 * u + i] = codes_f16(w, 0x04030401u);
+                        for (int k = 0; k < PP; ++k) pf[k][2 * u + i] = part[k];
+                        const uint32_t w = ld16(v + 2 * i * RB) | ld16(v + (2 * i + 1) * RB) << 16;
+                        vf[0][2 * u + i] = codes_bf16<0, 2>(w);
+                        vf[1][2 * u + i] = codes_bf16<1, 3>(w);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int k = PARTS - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
+                    for (int k = PP - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
             }
             settle();
         }
@@ -404,12 +388,12 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
             float sc[8];
             f4v acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-            for (int k = PARTS - 1; k >= 0; --k)
+            for (int k = QP - 1; k >= 0; --k)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const u4v qf = s_q[b][k][lane];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) acc[u] = mfma16<BF>(kf[u][b], qf, acc[u]);
+                    for (int u = 0; u < 2; ++u) acc[u] = mfma16<QBF>(kf[u][b], qf, acc[u]);
                 }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = acc[i >> 2][i & 3] * qs;
@@ -422,13 +406,13 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                 }
             }
             soften(sc);
-            u4v pf[PARTS];
+            u4v pf[PP];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t part[PARTS];
-                split_pair<BF, PARTS>(sc[2 * i], sc[2 * i + 1], part);
+                uint32_t part[PP];
+                split_pair<BF, PP>(sc[2 * i], sc[2 * i + 1], part);
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) pf[k][i] = part[k];
+                for (int k = 0; k < PP; ++k) pf[k][i] = part[k];
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -442,7 +426,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int k = PARTS - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
+                    for (int k = PP - 1; k >= 0; --k) o[b][j] = mfma16<BF>(vf[j], pf[k], o[b][j]);
             }
             place(t + kWaves);
         }
@@ -459,7 +443,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) s_o[wave][m][32 * b + 8 * g + 2 * i + j] = o[b][j][i] * (Q8 ? vlim : 1.0f);
+            for (int j = 0; j < 2; ++j) s_o[wave][m][32 * b + 8 * g + 2 * i + j] = o[b][j][i];
     if (g == 0) s_m[wave][m] = mx, s_l[wave][m] = l;
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {

@@ -28,9 +28,12 @@
 // latter's results were neighbours of the right ones.)  fp32 queries and P are split
 // into two fp16 parts (three bf16 ones for a bf16 cache), and the values of Q8_0
 // rows, d times a code, into two fp16 parts, which hold them exactly: three products
-// of parts instead of one, and with bf16 queries two for scores and three for P V.  Q8_0 values are staged times a power of two, the
-// same for all keys of a tile (and one for its values), that keeps the largest
-// below 2^15.
+// of parts instead of one, and with bf16 queries two for scores and three for P V.
+// Q8_0 keys and values are staged times powers of two that keep the largest below
+// 2^15: one for a tile's keys, one for each 32 values of all keys so far, so that a
+// block that is small beside others loses nothing; keys and values 2^16 and more
+// below the largest they share one with are held to 2^-38 of that, the parts'
+// smallest step, as P is to 2^-39 of a row's largest.
 //
 // Bound: nothing alone; the matrix unit is busy for 40% of the time.  A prompt
 // of 8191 tokens (bf16 queries, 32 heads, of 128, on 8 of an fp16 cache; 550
@@ -86,6 +89,15 @@ struct Staged {
     uint32_t vd[VT][Q8 ? 8 : 1];
 };
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+// What the lanes of block b (from lane 8 b on) hold.
+__device__ __forceinline__ float of_block(float x, int b) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 8 * b));
+}
+
 // The largest group of operands, up to `most`, that n of them divide into.
 constexpr int group_of(int n, int most) { return n % most ? group_of(n, most - 1) : most; }
 // Parts of Q and of P, and rows of a wave.
@@ -112,8 +124,11 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     constexpr int BUFS = !Q8 && 2 * (K_BYTES + V_BYTES) * (8 / W) <= 150 * 1024 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) uint8_t s_k[BUFS * AP][K_BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t s_v[BUFS * AP][V_BYTES];
-    __shared__ float s_big[2][W][2];  // of a tile, a wave's keys each: the largest |d| of K and V (Q8_0),
-    __shared__ int s_page[2][W];      // and whether they have a page
+    // of a tile, twice: the largest |d| of the keys that each wave staged (Q8_0), whether they have a page,
+    // and the largest |d| of the values, of each 8 keys and 32 values
+    __shared__ float s_big[2][W];
+    __shared__ int s_page[2][W];
+    __shared__ __attribute__((aligned(16))) float s_vd[Q8 ? 2 : 1][NB][8];
 
     // a long sequence's last tiles see the most keys: they go first.  The
     // heads of a tile are neighbours, so (with 8 of them) each XCD keeps to one
@@ -215,7 +230,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 #pragma unroll
         for (int i = 0; i < VL; ++i) o[c][i] = 0.f;
     float mx = -INFINITY, mref = 0.f, l = 0.f;
-    float vlim = 0x1p-30f;  // Q8_0: a power of two that no |d| so far is above
+    int vex = -30;  // Q8_0: 2^vex is above every |d| so far of the lane's block of values, lane / 8 % NB
 
     int64_t my_row = -1;  // lane i: where the wave's keys of tile i from here on begin in the cache, or -1
     St st;
@@ -248,12 +263,12 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         return (row >= 0) & (((key >= at.low) & (key < at.end)) | (key < at.pre));
     };
     // Loads the wave's keys and values of tile t, which begin at cache row `row`; the largest |d| of the Q8_0 blocks of K
-    // and of V that this lane holds.
-    auto fetch = [&](int t, int64_t row) -> float2 {
+    // that this lane holds.
+    auto fetch = [&](int t, int64_t row) -> float {
         const int key0 = key_at(t);
         const uint8_t* kbase = a.c.k + max(row, (int64_t)0) * RB;  // uniform, with 32-bit offsets of the lanes
         const uint8_t* vbase = a.c.v + max(row, (int64_t)0) * RB;
-        float2 big = make_float2(0.f, 0.f);
+        float big = 0.f;
 #pragma unroll
         for (int i = 0; i < St::KT; ++i) {
             const uint32_t task = lane + 64 * i;
@@ -306,12 +321,12 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         if constexpr (Q8) {
 #pragma unroll
             for (int i = 0; i < St::KT; ++i)
-                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB) big.x = fmaxf(big.x, fabsf(h2f(st.k[i][0])));
+                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB) big = fmaxf(big, fabsf(h2f(st.k[i][0])));
+            static_assert(St::VT == 1, "a lane stages values of one block");
+            float vd = 0.f;
 #pragma unroll
-            for (int i = 0; i < St::VT; ++i)
-                if (KPW * NB % 64 == 0 || lane + 64 * i < KPW * NB)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) big.y = fmaxf(big.y, fabsf(h2f(st.vd[i][j])));
+            for (int j = 0; j < 8; ++j) vd = fmaxf(vd, fabsf(h2f(st.vd[0][j])));
+            if (lane < KPW * NB && lane % 8 == 0) s_vd[t & 1][lane / 8 % NB][KPW / 8 * wave + lane / (8 * NB)] = vd;
         }
         return big;
     };
@@ -388,39 +403,36 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     // Loads tile t, and tells the other waves about it before the barrier that all pass before it is stored.
     auto begin = [&](int t) {
         const int64_t row = row_of(t);
-        float2 big = fetch(t, row);
+        float big = fetch(t, row);
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 1; k < 64; k <<= 1)
-                big.x = fmaxf(big.x, __shfl_xor(big.x, k)), big.y = fmaxf(big.y, __shfl_xor(big.y, k));
+            for (int k = 1; k < 64; k <<= 1) big = fmaxf(big, __shfl_xor(big, k));
         }
-        if (lane == 0) {
-            s_big[t & 1][wave][0] = big.x, s_big[t & 1][wave][1] = big.y;
-            s_page[t & 1][wave] = row >= 0;
-        }
+        if (lane == 0) s_big[t & 1][wave] = big, s_page[t & 1][wave] = row >= 0;
     };
     // Q8_0: powers of two, the same in every wave, of tile t's K (the limit is
-    // returned), and of V so far (vlim: raised where tile t needs it, o with it).
-    // Values are staged as 2^8 d code / limit < 2^15.
+    // returned), and of each 32 values so far (2^vex: raised where tile t needs it,
+    // o with it).  Both are staged as 2^8 d code / limit < 2^15.
     auto k_limit = [&](int t) {
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i][0]);
+        for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i]);
         int ex = 0;
         frexpf(fminf(big, 65504.0f), &ex);
         return ldexpf(1.0f, ex);
     };
     auto v_limit = [&](int t) {
-        float big = 0.f;
+        float big = s_vd[t & 1][lane / 8 % NB][lane % 8];
+        big = fmaxf(big, dpp<0xB1>(big));   // lane ^ 1
+        big = fmaxf(big, dpp<0x4E>(big));   // lane ^ 2
+        big = fmaxf(big, dpp<0x141>(big));  // 7 - lane, of each 8
+        // (fp16 numbers are no subnormals in fp32)
+        const int ex = max(vex, min((__builtin_bit_cast(int, big) >> 23) - 126, 16));
+        if (__any(ex > vex)) {
+            const float down = ldexpf(1.0f, vex - ex);
+            vex = ex;
 #pragma unroll
-        for (int i = 0; i < W; ++i) big = fmaxf(big, s_big[t & 1][i][1]);
-        if (big > vlim) {
-            int ex = 0;
-            frexpf(fminf(big, 65504.0f), &ex);
-            const float lim = ldexpf(1.0f, ex), down = vlim / lim;
-            vlim = lim;
-#pragma unroll
-            for (int c = 0; c < NO; ++c) o[c] *= down;
+            for (int c = 0; c < NO; ++c) o[c] *= of_block(down, R * c / 32);
         }
     };
 
@@ -438,7 +450,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     };
     float s[R];
     // From the products of tile t to scores (f s, times log2 e), masked; raises
-    // the running maximum where they pass it by 7.
+    // the running maximum where they pass it by kSlack.
     auto soften = [&](int t, float& f) {
         const int kb = kKeys * (t < n_pre ? t : t - n_pre + w0);
         bool page[4];  // of each 16 keys
@@ -468,13 +480,13 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         float big = s[0];
 #pragma unroll
         for (int i = 1; i < R; ++i) big = fmaxf(big, s[i]);
-        if (__any(big * f > mx + 7.0f)) {
+        if (__any(big * f > mx + kSlack)) {
             if constexpr (R == 16) big = fmaxf(big, __shfl_xor(big, 16));
             big = fmaxf(big, __shfl_xor(big, 32)) * f;
             const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
             const float down = __builtin_amdgcn_exp2f(mx - ref);
             mx = top;
-            mref = ref - 8.0f;
+            mref = ref - p_top<BF>();
             l *= down;
 #pragma unroll
             for (int c = 0; c < NO; ++c) o[c] *= down;
@@ -491,7 +503,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             v_limit(t);
             f *= lim * 0x1p-8f;
             store_k(0x1p8f / lim, buf);
-            store_v(0x1p8f / vlim, buf);
+            store_v(ldexpf(1.0f, 8 - vex), buf);
         } else {
             store_k(1.0f, buf);
             store_v(1.0f, buf);
@@ -574,7 +586,8 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     l += __shfl_xor(l, 32);
     if (R * wave + r >= rows) return;
     const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
-    const float unit = Q8 ? vlim * 0x1p-8f : 1.0f;
+    const float lane_unit = Q8 ? ldexpf(1.0f, vex - 8) : 1.0f;
+    auto unit = [&](int c) { return Q8 ? of_block(lane_unit, R * c / 32) : 1.0f; };
     if (a.splits && h == 0 && w.split == 0)
         join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * a.slots + R * wave + r};
     // accumulator c, value i: value R c + 8 (i / 4) + 4 h + i % 4 of the row
@@ -583,19 +596,22 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         float* ml = a.work + a.parts * D;
         if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
 #pragma unroll
-        for (int c = 0; c < NO; ++c)
+        for (int c = 0; c < NO; ++c) {
+            const float u = unit(c);
 #pragma unroll
             for (int i = 0; i < VL; i += 4)
                 *reinterpret_cast<f4v*>(a.work + part * D + R * c + 2 * i + 4 * h) =
-                    f4v{o[c][i] * unit, o[c][i + 1] * unit, o[c][i + 2] * unit, o[c][i + 3] * unit};
+                    f4v{o[c][i] * u, o[c][i + 1] * u, o[c][i + 2] * u, o[c][i + 3] * u};
+        }
         return;
     }
-    const float inv = (l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l) * unit;
+    const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;
 #pragma unroll
     for (int c = 0; c < NO; ++c)
 #pragma unroll
         for (int i = 0; i < VL; i += 4) {
-            const float x0 = o[c][i] * inv, x1 = o[c][i + 1] * inv, x2 = o[c][i + 2] * inv, x3 = o[c][i + 3] * inv;
+            const float w = inv * unit(c);
+            const float x0 = o[c][i] * w, x1 = o[c][i + 1] * w, x2 = o[c][i + 2] * w, x3 = o[c][i + 3] * w;
             const int64_t e = row * D + R * c + 2 * i + 4 * h;
             if constexpr (XB) {
                 uint32_t w0[1], w1[1];

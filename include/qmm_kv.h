@@ -142,7 +142,12 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
  *           aligned; may be NULL when that is 0.  Calls that may run at the
  *           same time need one each; contents need not be kept.
  * Fp32 results are as exact as a product in fp32, bf16 results are these
- * rounded once, whichever kernels compute them.  What lies in the cache at
+ * rounded once, whichever kernels compute them, with one reserve: over F16 and
+ * Q8_0 rows the products are made of 16-bit parts, whose smallest step is 2^-38
+ * of the largest query value of a head, of the largest weight of a row, and of
+ * the largest key of a tile of 64 (and the largest value among 32 of any key
+ * that the rows of a tile see), so that what is more than 2^16 smaller than these
+ * keeps fewer bits than fp32's, and what is 2^20 smaller still 18.  What lies in the cache at
  * places that no row of the call sees has no effect, infinities and NaN
  * included; visible keys and values have to be finite.  Batches whose grids
  * would pass 2^32 work-items are refused (QMM_ERR_SHAPE). */
