@@ -30,8 +30,7 @@ UNITS = {
     "probe.hip": [],
     # stored cache rows are defined to the bit, as the codec's blocks are
     "kv_append.hip": ["-ffp-contract=off"],
-    # scores are no NaN unless the inputs are: no maximum has to quiet one first
-    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-fno-honor-nans"]
+    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
        for kind in ("split", "tile_narrow", "tile_wide") for cache in ("q8_0", "f16", "bf16")},
     "attn_join.hip": [],
     "qmm.cpp": [],

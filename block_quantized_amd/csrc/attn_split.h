@@ -195,7 +195,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int u = i >> 2, key = kb + 16 * u + 4 * g + (i & 3);
-                // without branches: this compiler has dropped the assignment where they were nested
+                // (without branches: ROCm 7.2's compiler keeps sc as one tuple of registers, and where the assignment
+                // stood in nested branches it copied the tuple as it was before over it, with and without honoured NaNs)
                 const bool seen =
                     (key < at.len) & (r0[u] >= 0) & (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
                 sc[i] = seen ? sc[i] : -INFINITY;
