@@ -60,9 +60,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int each) {
         const int mine = thread / LANES, e = 4 * (thread % LANES);
         f4v sum = {0.f, 0.f, 0.f, 0.f};
         float den = 0.f;
-        if (mine < AT && top != -INFINITY) {
+        if (mine < AT) {
             for (int z = mine; z < j.splits; z += AT) {
-                const float f = __builtin_amdgcn_exp2f(ml[2 * step * z] - top);
+                // (a part without a maximum has seen no key, or NaN alone, which stays)
+                const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * step * z] - top);
                 den += f * ml[2 * step * z + 1];
                 sum += f * *reinterpret_cast<const f4v*>(part + step * z * D + e);
             }
