@@ -332,7 +332,8 @@ def _int32(what: str, t, *shape):
 
 class KVCache:
     """The paged cache of one layer: tensors k and v of n_pages x n_kv x
-    page_size rows (uint8 Q8_0 blocks, float16 or bfloat16; see qmm_kv.h)."""
+    page_size rows (Q8_0 blocks as uint8, float16 or bfloat16, or the bytes of
+    these as uint8; see qmm_kv.h)."""
 
     def __init__(self, k, v, type: int, n_kv: int, head_dim: int, page_size: int):
         page = qmm_kv_bytes(type, n_kv, head_dim, page_size, 1)
@@ -343,6 +344,10 @@ class KVCache:
             _refuse(QMM_ERR_SHAPE, f"KVCache: k and v have to be whole pages of {page} bytes, as many of each")
         if not k.is_contiguous() or not v.is_contiguous():
             _refuse(QMM_ERR_UNSUPPORTED, "KVCache: k and v have to be contiguous")
+        torch = _need_torch()
+        own = {QMM_F16: torch.float16, QMM_BF16: torch.bfloat16}.get(type, torch.uint8)
+        if k.dtype not in (own, torch.uint8) or v.dtype not in (own, torch.uint8):
+            _refuse(QMM_ERR_UNSUPPORTED, f"KVCache: k and v have to hold {own} values, or bytes (uint8)")
         self.dev = _device_of("KVCache", k, v)
         self.k, self.v, self.type = k, v, type
         self.n_kv, self.head_dim, self.page_size, self.n_pages = n_kv, head_dim, page_size, size // page
