@@ -395,9 +395,13 @@ class Rope:
     def __init__(self, freqs, pairing: int, pos=None, sections=None):
         if freqs.dtype != _need_torch().float64 or not freqs.is_contiguous() or freqs.dim() != 1:
             _refuse(QMM_ERR_SHAPE, "Rope: freqs has to be a contiguous float64 vector")
+        if pairing not in (QMM_ROPE_PAIRS, QMM_ROPE_HALVES):
+            _refuse(QMM_ERR_UNSUPPORTED, "Rope: pairing has to be QMM_ROPE_PAIRS or QMM_ROPE_HALVES")
         axes = len(sections) if sections is not None else 1
         if not 1 <= axes <= 4:
             _refuse(QMM_ERR_SHAPE, "Rope: 1 to 4 axes")
+        if sections is not None and not all(0 <= n <= freqs.numel() for n in sections):  # ctypes would cut them
+            _refuse(QMM_ERR_SHAPE, "Rope: the pairs of the axes have to be those of freqs")
         if pos is not None:
             if pos.dim() == 1:
                 pos = pos[None]

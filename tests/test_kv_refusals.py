@@ -16,3 +16,15 @@ def test_pools_of_another_type(type, dtype):
         assert e.value.code == Q.QMM_ERR_UNSUPPORTED
     with pytest.raises(Q.QmmError, match="one GPU"):  # bytes are taken; what is wrong with them is where they lie
         Q.KVCache(right, right, type, 1, 64, 16)
+
+
+def test_rotations_that_ctypes_would_cut():
+    f = torch.zeros(4, dtype=torch.float64)
+    for pairing in (2, -1, 2 ** 32, 2 ** 32 + 1):
+        with pytest.raises(Q.QmmError, match="pairing") as e:
+            Q.Rope(f, pairing)
+        assert e.value.code == Q.QMM_ERR_UNSUPPORTED
+    for sections in ([2 ** 32 + 2, 2], [-1, 5], [5, 0]):
+        with pytest.raises(Q.QmmError, match="axes") as e:
+            Q.Rope(f, 0, sections=sections)
+        assert e.value.code == Q.QMM_ERR_SHAPE
