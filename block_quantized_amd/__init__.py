@@ -459,13 +459,19 @@ def _xtype(what: str, dtype):
     return QMM_BF16
 
 
+def _no_grad(what: str, *tensors):
+    if _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        _refuse(QMM_ERR_UNSUPPORTED, f"{what}: no gradients are computed; detach the inputs or use torch.no_grad()")
+
+
 def _new_out(x):
     return _torch.empty_like(x, memory_format=_torch.contiguous_format)
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=None, stream=None):
     """Stores k (rotated) and v (tokens, n_kv, head_dim) in the cache, and
-    returns q (tokens, n_q, head_dim) rotated, in q_out if given."""
+    returns q (tokens, n_q, head_dim) rotated, in q_out if given.  No
+    gradients: inputs that require them are refused where torch records them."""
     torch = _torch or _need_torch()
     dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, k.dtype
     same = batch.dev == dev and k.get_device() == dev and v.get_device() == dev and v.dtype == dtype
@@ -489,6 +495,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=Non
             _refuse(QMM_ERR_SHAPE, "kv_append: pos has to name a position for every token")
     if not same:
         _refuse(QMM_ERR_UNSUPPORTED, "kv_append: tensors have to lie on one GPU and be of one type")
+    _no_grad("kv_append", k, v, q, q_out)
     xtype = _xtype("kv_append", dtype)
     if stream is not None or torch.cuda.current_device() != dev:
         handle, where = _elsewhere(dev, stream)
@@ -512,7 +519,7 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
          prefix=None, algo: int = 0, out=None, stream=None):
     """Attention of q (tokens, n_q, head_dim) over the cache -> (tokens, n_q,
     head_dim), in out if given.  scale defaults to head_dim ** -0.5.  Rows of
-    no sequence are not written."""
+    no sequence are not written.  No gradients, as kv_append."""
     torch = _torch or _need_torch()
     dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, q.dtype
     same = batch.dev == dev and q.get_device() == dev
@@ -532,6 +539,7 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
         _refuse(QMM_ERR_UNSUPPORTED, "attn: tensors have to lie on one GPU, and out be of q's type")
     if not 0 <= window < 1 << 31 or not 0 <= algo <= 2:  # ctypes would take their low 32 bits
         _refuse(QMM_ERR_UNSUPPORTED, "attn: window has to be 0 to 2^31 - 1, algo 0 to 2")
+    _no_grad("attn", q, slopes, out)
     xtype = _xtype("attn", dtype)
     opts = ctypes.byref(qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes),
                                       _ptr(prefix)))
