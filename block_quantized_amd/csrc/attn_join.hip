@@ -57,13 +57,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int each) {
         for (int z = lane; z < j.splits; z += 64) top = fmaxf(top, ml[2 * step * z]);
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+        if (top == -INFINITY) top = 0.f;  // no part has seen a key, or one of NaN, which stays
         const int mine = thread / LANES, e = 4 * (thread % LANES);
         f4v sum = {0.f, 0.f, 0.f, 0.f};
         float den = 0.f;
         if (mine < AT) {
             for (int z = mine; z < j.splits; z += AT) {
-                // (a part without a maximum has seen no key, or NaN alone, which stays)
-                const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * step * z] - top);
+                const float f = __builtin_amdgcn_exp2f(ml[2 * step * z] - top);
                 den += f * ml[2 * step * z + 1];
                 sum += f * *reinterpret_cast<const f4v*>(part + step * z * D + e);
             }
