@@ -25,7 +25,7 @@ __device__ __forceinline__ void put(const AttnArgs& a, int64_t row, int e, f4v s
 // few rows the four wavefronts of a workgroup share each (WHOLE); from 2048 on
 // each has `each` rows of its own, whose parts it looks up together (a batch of
 // thousands of short sequences has few that are split).
-// Bound: latency, a chain of three loads.  32 rows of 64 splits 6.2 us, 2048 of
+// Bound: latency, a chain of three loads.  32 rows of 64 splits 6.3 us, 2048 of
 // 3 to 6 splits 6.4 (6.8 with a workgroup a row; 45000 of 2 took 46 us more so).
 template <int D, bool XB, bool WHOLE>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int each) {

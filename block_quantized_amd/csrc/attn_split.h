@@ -29,11 +29,11 @@
 // the parts' smallest step.
 //
 // Bound: reading the cache.  fp32 queries, 32 heads, of 128 values, on 8 of the
-// cache's: one sequence of 131k keys in Q8_0 (285 MB) 61 us, 4.7 TB/s; 64 of
-// 8k to 16k (1714 MB) 316-347 us, 4.9-5.4; 13 of 750 to 1500 in bf16, each head
-// with its own (244 MB) 43 us, 5.7; 32 of 2k to 4k, 256-wide in fp16 with bf16
+// cache's: one sequence of 131k keys in Q8_0 (285 MB) 64 us, 4.5 TB/s; 64 of
+// 8k to 16k (1714 MB) 314-371 us, 4.6-5.5; 13 of 750 to 1500 in bf16, each head
+// with its own (244 MB) 42 us, 5.8; 32 of 2k to 4k, 256-wide in fp16 with bf16
 // queries (814 MB) 153 us, 5.3.  A read of 1 GiB that computes nothing reaches
-// 5.5.  In Q8_0 the vector unit is busy for 58% of the time (codes to fp16, P d
+// 5.5.  In Q8_0 the vector unit is busy for 72% of the time (codes to 16 bits, P d
 // split).  Slower, each against its time then: loads past the caches (172 us for
 // the last), unaligned loads of whole blocks with transposing LDS reads (418 ->
 // 468), all products before all scales (254 -> 277), four waves a SIMD (spills).

@@ -35,18 +35,19 @@
 // below the largest they share one with are held to 2^-38 of that, the parts'
 // smallest step, as P is to 2^-39 of a row's largest.
 //
-// Bound: nothing alone; the matrix unit is busy for 40% of the time.  A prompt
-// of 8191 tokens (bf16 queries, 32 heads, of 128, on 8 of an fp16 cache; 550
-// GFLOP) takes 627-660 us, 0.83-0.88 PFLOP/s of the 1.33 that a large product of
-// matrices reaches here; with three products each, 2048 tokens over Q8_0 (34
-// GFLOP, 103 multiplied) 146-160 us.  Of the former's time the operands' LDS
-// reads cost 29%, the staging 20% (loads 12, writes 7), the masks' and maxima's
-// pass 6, the exponentials 2 (each left out in turn).  Tried and no faster: the next tile's scores
-// multiplied between a tile's exponentials (647 -> 649: registers for it leave
-// no room to read operands earlier), the next tile written among the products
-// (665 -> 677), 256 rows a workgroup (665 -> 658, and 200 -> 215 for four
-// prompts of 2200), 16 rows a wave (636 -> 933), light and heavy row tiles
-// paired (657 -> 698), s_setprio around the products (no change).
+// Bound: nothing alone; the matrix unit and the vector unit are busy for 45% of the
+// time each.  A prompt of 8191 tokens (bf16 queries, 32 heads, of 128, on 8 of an
+// fp16 cache; 550 GFLOP, 825 multiplied) takes 850 us, 0.97 PFLOP/s multiplied of
+// the 1.33 that a large product of matrices reaches here; with three products each,
+// 2048 tokens over Q8_0 (34 GFLOP, 103 multiplied) 152 us.  Of the former's time
+// with P in one part (630 us) the operands' LDS reads cost 29%, the staging 20%
+// (loads 12, writes 7), the masks' and maxima's pass 6, the exponentials 2 (each
+// left out in turn).  Tried then and no faster: the next tile's scores multiplied
+// between a tile's exponentials (647 -> 649: registers for it leave no room to read
+// operands earlier), the next tile written among the products (665 -> 677), 256 rows
+// a workgroup (665 -> 658, and 200 -> 215 for four prompts of 2200), 16 rows a wave
+// (636 -> 933), light and heavy row tiles paired (657 -> 698), s_setprio around the
+// products (no change).
 #pragma once
 
 #include "attn_common.h"

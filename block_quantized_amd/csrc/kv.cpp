@@ -119,14 +119,16 @@ int tile_tokens(int rows, int chunk, int64_t each) {
 // waves' parts fill LDS; 6 less where nothing is joined) and 1 us for 1000 such
 // products of 64 values, the latter's some 9 us and 3 us a step, as many steps as
 // a row tile sees tiles of keys, times the rounds of 512 workgroups; or, their
-// keys split (128 row tiles at most), 22 us and 9.5 for each 512 steps.  Split against tile kernels, us: 1588 tokens, 14 heads on 2
-// of 64, fp32: 45, 56; 3 x 1078 of the same, bf16 over Q8_0: 71, 64; 2 x 892, 32
-// on 8 of 128: 90, 51; 397 behind 237, 32 heads of 128 each its own, fp32: 35,
-// 47; 314, 16 on 8 of 256, fp32: 37, 29; 462, 14 on 2 of 64: 22, 39; with a
-// window of 97, 3 x 1116: 36, 20; 328 behind 409, 32 on 8 of 128, fp32: 34, 48; 85
-// of 32 on 8 of 64: 8, 11.  Over 160 sizes drawn at random the choice costs 1.4%
-// (geometric mean) against the better one of each.  Below 48 rows a sequence most
-// of a tile is idle.
+// keys split (128 row tiles at most), 22 us and 9.5 for each 512 steps.  (That is an
+// estimate of both: two parts for heavy steps and the types' different steps are
+// not in it.)  Split against tile kernels, us: 1588 tokens, 14 heads on 2 of 64,
+// fp32 over bf16: 42, 53; 3 x 1078 of the same, bf16 over Q8_0: 68, 80; 2 x 892, 32
+// on 8 of 128, bf16 over Q8_0: 86, 68; 397 behind 237, 32 heads of 128 each its own,
+// fp32 over fp16: 32, 40; 314, 16 on 8 of 256, the same: 35, 28; 462, 14 on 2 of 64,
+// Q8_0: 19, 24; with a window of 97, 3 x 1116, bf16 over Q8_0: 33, 22; and wrong: 2 x
+// 654, 32 on 8 of 64, bf16: 32 (taken), 25; 124, 16 on 8 of 256, bf16 over Q8_0: 13,
+// 22 (taken).  Over 160 sizes drawn at random the choice costs 1.7% (geometric mean)
+// against the better one of each.  Below 48 rows a sequence most of a tile is idle.
 int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int n_q) {
     const int G = n_q / c->n_kv;
     const int64_t each = up_div(b->n_tokens, b->n_seqs), rows = up_div(b->n_tokens * G, b->n_seqs);
@@ -160,18 +162,21 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     // that the last of them end together (64 conversations of 8k to 16k keys: 397 us
     // with 512 workgroups, 362 with 1024, 338 with 2048, 340 with 2560); where that
     // leaves each below 2048 keys, among fewer, at least 512, two a CU (one of
-    // 131k keys, 8 heads: 76 us with 512, 88 with 2048), less one a row tile, which
-    // may add a part that is not full, so that all run at once (three a CU, two for
-    // heads above 128; us without, with: 10 sequences, 3341 keys, 8 heads of 256 in
-    // bf16: 89, 67; 7 of 9000 in Q8_0: 77, 59; 13 of 1400, 32 of 128: 57, 49).  A
-    // part keeps 128 keys, a tile a wave (one sequence of 1940: 14 us; with 256 keys
-    // 16, with 512 22).
+    // 131k keys, 8 heads: 76 us with 512, 88 with 2048), or as many as run at once
+    // (three a CU, two for heads above 128) less one a row tile, which may add a part
+    // that is not full, where these are 256 to 512 (us without, with, 32 heads of 128
+    // each its own over bf16, 1400 keys: 14 sequences 64, 57; 16: 68, 63; 24 of 3000, 16
+    // on 8 of 256: 150, 127; but 12: 51, 55).  Below 256 the gain is small either way (18
+    // of 1400: 79, 72; 72 of 8 heads: 50, 55).  A part keeps 128 keys, a tile a wave (one
+    // sequence of 1940: 14 us; with 256 keys 16, with 512 22).
     // Tile kernels split only what makes four parts and more of a row tile: fewer
     // cost in writing and joining what they save (us with two, without: 309 tokens
     // twice, 32 heads, 30 and 18; 602 tokens, a window of 17: 35 and 21).  Where a
     // step is long, that is for wide heads over Q8_0 rows and with fp32 queries over
-    // bf16 rows, two parts pay (2048 tokens, 16 heads on 4 of 256: Q8_0 168 and 224,
-    // with bf16 queries 111 and 139; bf16 rows 148 and 180; but fp16 rows 118, 112).
+    // bf16 rows, two parts pay (16 heads on 8 of 256, us without, with: Q8_0, fp32: 1024
+    // tokens 117, 86; 1500: 161, 133; 2048: 222, 165; 3000: 319, 325; bf16 rows, fp32: 96,
+    // 85; 130, 125; 179, 153; 258, 297; but fp32 over fp16 rows 62, 62; 83, 85; 112, 106;
+    // 166, 192).
     p.least = 4;
     const bool heavy = c->head_dim > 128 && (c->type == QMM_Q8_0 || (c->type == QMM_BF16 && xtype == QMM_F32));
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);

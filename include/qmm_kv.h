@@ -66,9 +66,9 @@ typedef struct {
     int32_t n_seqs;         /* 65536 at most                                   */
     int32_t table_width;    /* pages of a sequence at most, 2^30 tokens in all */
     int64_t n_tokens;       /* rows of q, k, v and out, below 2^23             */
-    int64_t max_kv;         /* largest kv_len, as far as known; 0: unknown.  It
-                               only decides how the work is split: results hold
-                               for any value                                   */
+    int64_t max_kv;         /* largest kv_len, as far as known; 0: unknown (the
+                               table's width counts).  It only decides how the
+                               work is split: results hold for any value       */
 } qmm_kv_batch;
 
 /* The rotation of positions: pair i of the first n_rot values of a head turns
@@ -150,7 +150,12 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
  * keeps fewer bits than fp32's, and what is 2^20 smaller still 18.  What lies in the cache at
  * places that no row of the call sees has no effect, infinities and NaN
  * included; visible keys and values have to be finite.  Batches whose grids
- * would pass 2^32 work-items are refused (QMM_ERR_SHAPE). */
+ * would pass 2^32 work-items are refused (QMM_ERR_SHAPE).
+ *
+ * The kernels are chosen, and the keys divided, by what a batch's sequences have
+ * on average.  Prompts beside single tokens over long caches belong in two calls
+ * on parts of the batch's arrays: 2048 tokens beside one over 131072 keys (Q8_0, 32
+ * heads on 8 of 128) take 9.1 ms in one, 0.15 + 0.07 in two. */
 int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,
              int64_t ldq, int n_q, void* out, void* work, size_t work_bytes, void* stream);
 
