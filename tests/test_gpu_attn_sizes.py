@@ -91,3 +91,46 @@ def test_largest_bf16_values(algo):
     out = R.attention64(q, b, ks, vs, 1, scale)[0]
     assert np.isfinite(got).all()
     assert np.linalg.norm((got - out) * 2.0 ** -120) <= 2.0 ** -18 * np.linalg.norm(out * 2.0 ** -120)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("cache", [R.Q8, R.F16, R.BF16])
+@pytest.mark.parametrize("what", ["queries", "keys"])
+@pytest.mark.parametrize("ratio", [1e4, 1e6])
+def test_queries_and_keys_of_different_sizes(algo, cache, what, ratio):
+    """Query values that are `ratio` times larger than a head's others and meet
+    keys of 0, or one key that is `ratio` times larger than its neighbours and
+    far from every query.  Parts of fp16 step by 2^-24 where the largest value x
+    is 2^13 or more, so each value is off by 2^-38 x at most, and a score by
+    scale 2^-38 x |k| (2-norm) / sqrt(3) in the root mean square, x being the
+    largest of the queries here, up to 4 ratio: a result by sqrt(2) of that (weights
+    above and below the line), and by less than 4 times its 2-norm bound over all
+    the rows looked at."""
+    g = synth.rng(103)
+    dim, n_q = 64, 2
+    b, c, kb, ks, vs = setup(g, [(1, 100), (40, 90)], 16, cache, 1, dim)
+    q = R.as_type(synth.normal_f32(g, (b.N, n_q, dim)), R.F32)
+    host = c.k.cpu().numpy()
+    for s, L in enumerate(b.len):
+        for j in range(L):
+            k = ks[s][j].astype(np.float32)
+            if what == "queries":
+                k[:, :32] = 0.0
+            elif j == 30:
+                k[:], k[:, 0] = 0.0, -ratio / 100
+            else:
+                k[:, :32] /= 100
+            row = R.stored_rows(k, cache)
+            host[b.table[s, j // 16], :, j % 16] = row
+            ks[s][j] = R.row_values(row, cache, dim)
+    c.k.copy_(torch.from_numpy(host))
+    if what == "queries":
+        q[..., :32] *= np.float32(ratio)
+    else:
+        q[..., 0] = 8.0  # the large key's score is -100 or less
+    scale = np.float64(np.float32(dim ** -0.5))
+    got = to_cpu(Q.attn(c, kb, to_gpu(q), scale=float(scale), algo=algo))
+    out = R.attention64(q, b, ks, vs, 1, scale)[0]
+    err = block_errors(got, out)
+    step = 4 * np.sqrt(2 / 3) * scale * 2.0 ** -38 * np.abs(q).max() * max(np.linalg.norm(k[:, 0], axis=-1)[:30].max() for k in ks)
+    assert err.max() <= 2.0 ** -18 + step, (err.max(), np.unravel_index(err.argmax(), err.shape))
