@@ -1,21 +1,23 @@
 """Python binding of libqmm, the gfx950 GGUF block-quantized matrix product.
 
 Argument marshalling only: every function named ``qmm_*`` forwards to the C
-function of the same name in ``libqmm.so`` (declared in ``include/qmm.h`` and
-``include/qmm_probe.h`` and ``include/qmm_kv.h``).
+function of the same name in ``libqmm.so`` (declared in ``include/qmm.h``,
+``include/qmm_probe.h``, ``include/qmm_kv.h`` and ``include/qmm_logits.h``).
 Device buffers may be passed as torch tensors (their ``data_ptr()`` is used)
 or as integer device addresses; ``stream`` defaults to torch's current
 stream.  The ``qmm_*`` functions return the C status code.  The helpers
 below them (``quantize_act``, ``dequantize``, ``mul_mat`` ...) allocate their
 outputs with torch and raise :class:`QmmError` on a non-zero status.  The
-key-value cache has three plain holders of tensors (:class:`KVCache`,
-:class:`KVBatch`, :class:`Rope`) and the helpers :func:`kv_append` and
-:func:`attn` on them.
+key-value cache has plain holders of tensors (:class:`KVCache`,
+:class:`KVBatch`, :class:`Rope`, :class:`KVTree`, :class:`KVLayers`) and the
+helpers :func:`kv_append`, :func:`attn`, :func:`kv_copy` and
+:func:`kv_compact` on them; :func:`logprobs` reads a head's logits.
 
 There is no fallback: if ``libqmm.so`` is missing, loading fails loudly.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -56,6 +58,10 @@ class qmm_attn_opts(ctypes.Structure):
                 ("algo", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
 
 
+class qmm_kv_tree(ctypes.Structure):
+    _fields_ = [("seen", ctypes.c_void_p), ("depth", ctypes.c_void_p), ("words", ctypes.c_int32)]
+
+
 class QmmError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {qmm_strerror(code)} ({code})")
@@ -89,6 +95,13 @@ def lib() -> ctypes.CDLL:
             "qmm_attn": (I, [P, P, P, I, P, I64, I, P, P, SZ, P]),
             "qmm_attn_work": (SZ, [P, P, P, I, I]),
             "qmm_attn_choice": (I, [P, P, I, I]),
+            "qmm_kv_tree_build": (I, [P, P, P, P, P]),
+            "qmm_attn_tree": (I, [P, P, P, P, I, P, I64, I, P, P, SZ, P]),
+            "qmm_attn_tree_work": (SZ, [P, P, P, I, I]),
+            "qmm_kv_copy": (I, [P, I, P, P, P, I64, P]),
+            "qmm_kv_compact": (I, [P, I, P, I, I, P, P, P, I, P, P]),
+            "qmm_logprobs": (I, [I, P, I64, I64, I64, ctypes.c_float, ctypes.c_float, P, I, P, P, I, P, P, P, SZ, P]),
+            "qmm_logprobs_work": (SZ, [I, I64, I64, I]),
             "qmm_strerror": (ctypes.c_char_p, [I]),
             "qmm_probe_read": (I, [P, I64, P, I, P]),
             "qmm_probe_mfma": (I, [I, I64, P, P]),
@@ -106,7 +119,8 @@ def lib() -> ctypes.CDLL:
 EXPORTED = ("qmm_block_size", "qmm_block_bytes", "qmm_row_bytes", "qmm_vec_dot_type", "qmm_quantize_act",
             "qmm_quantize", "qmm_dequantize", "qmm_mul_mat", "qmm_mul_mat_algo", "qmm_mul_mat_multi",
             "qmm_mul_mat_choice", "qmm_kv_bytes", "qmm_rope_freqs", "qmm_kv_append", "qmm_attn", "qmm_attn_work",
-            "qmm_attn_choice",
+            "qmm_attn_choice", "qmm_kv_tree_build", "qmm_attn_tree", "qmm_attn_tree_work", "qmm_kv_copy",
+            "qmm_kv_compact", "qmm_logprobs", "qmm_logprobs_work",
             "qmm_strerror", "qmm_probe_read", "qmm_probe_mfma", "qmm_probe_mfma_ops",
             "qmm_probe_mfma16", "qmm_probe_mfma16_ops")
 
@@ -207,6 +221,40 @@ def qmm_attn_work(cache, batch, opts, xtype, n_q) -> int:
 
 def qmm_attn_choice(cache, batch, xtype, n_q) -> int:
     return lib().qmm_attn_choice(_ref(cache), _ref(batch), xtype, n_q)
+
+
+def qmm_kv_tree_build(batch, parents, tree, pos, stream=None) -> int:
+    return lib().qmm_kv_tree_build(_ref(batch), _ptr(parents), _ref(tree), _ptr(pos), _stream(stream))
+
+
+def qmm_attn_tree(cache, batch, tree, opts, xtype, q, ldq, n_q, out, work, work_bytes, stream=None) -> int:
+    return lib().qmm_attn_tree(_ref(cache), _ref(batch), _ref(tree), _ref(opts), xtype, _ptr(q), ldq, n_q, _ptr(out),
+                               _ptr(work), work_bytes, _stream(stream))
+
+
+def qmm_attn_tree_work(cache, batch, opts, xtype, n_q) -> int:
+    return lib().qmm_attn_tree_work(_ref(cache), _ref(batch), _ref(opts), xtype, n_q)
+
+
+def qmm_kv_copy(caches, count, src, dst, rows, n, stream=None) -> int:
+    """caches: a ctypes array of qmm_kv_cache (or None)."""
+    return lib().qmm_kv_copy(caches, count, _ptr(src), _ptr(dst), _ptr(rows), n, _stream(stream))
+
+
+def qmm_kv_compact(caches, count, table, n_seqs, table_width, first, keep, n_keep, width, kv_len, stream=None) -> int:
+    return lib().qmm_kv_compact(caches, count, _ptr(table), n_seqs, table_width, _ptr(first), _ptr(keep), _ptr(n_keep),
+                                width, _ptr(kv_len), _stream(stream))
+
+
+def qmm_logprobs(xtype, logits, ld, rows, vocab, scale, softcap, tokens, n_tokens, logp, entropy, n_top, top_ids, top_logp,
+                 work, work_bytes, stream=None) -> int:
+    return lib().qmm_logprobs(xtype, _ptr(logits), ld, rows, vocab, scale, softcap, _ptr(tokens), n_tokens, _ptr(logp),
+                              _ptr(entropy), n_top, _ptr(top_ids), _ptr(top_logp), _ptr(work), work_bytes,
+                              _stream(stream))
+
+
+def qmm_logprobs_work(xtype, rows, vocab, n_top) -> int:
+    return lib().qmm_logprobs_work(xtype, rows, vocab, n_top)
 
 
 def qmm_probe_read(src, nbytes, sink, workgroups=0, stream=None) -> int:
@@ -515,11 +563,41 @@ def _append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out, handl
     return q_out
 
 
+class KVTree:
+    """The new tokens of a batch as trees of drafts: parents (int32, n_tokens)
+    names each token's parent by its place among the new tokens of its
+    sequence, before its own; -1: none.  max_new: the most new tokens that a
+    sequence has (at most 1024; all of the batch's unless given).  pos (1 x
+    n_tokens) are the tokens' positions, for :class:`Rope`."""
+
+    def __init__(self, batch: KVBatch, parents, max_new=None, stream=None):
+        torch = _need_torch()
+        n = batch.n_tokens
+        _int32("KVTree: parents", parents, n)
+        if _device_of("KVTree", parents) != batch.dev:
+            _refuse(QMM_ERR_UNSUPPORTED, "KVTree: parents have to lie on the batch's GPU")
+        most = min(n, 1 << 30) if max_new is None else max_new
+        if not 1 <= most <= 1024:
+            _refuse(QMM_ERR_SHAPE, "KVTree: max_new, the new tokens of a sequence, has to be 1 to 1024")
+        self.dev, self.n_tokens, self.words = batch.dev, n, -(-most // 64)
+        handle, where = _elsewhere(self.dev, stream)
+        with where:
+            self.seen = torch.empty((n, self.words), dtype=torch.int64, device=parents.device)
+            self.depth = torch.empty(n, dtype=torch.int32, device=parents.device)
+            self.pos = torch.empty((1, n), dtype=torch.int32, device=parents.device)
+            self.c = qmm_kv_tree(self.seen.data_ptr(), self.depth.data_ptr(), self.words)
+            self.ref = ctypes.byref(self.c)
+            _check(lib().qmm_kv_tree_build(batch.ref, parents.data_ptr(), self.ref, self.pos.data_ptr(), handle),
+                   "qmm_kv_tree_build")
+
+
 def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, window: int = 0, slopes=None,
-         prefix=None, algo: int = 0, out=None, stream=None):
+         prefix=None, algo: int = 0, out=None, stream=None, tree=None):
     """Attention of q (tokens, n_q, head_dim) over the cache -> (tokens, n_q,
-    head_dim), in out if given.  scale defaults to head_dim ** -0.5.  Rows of
-    no sequence are not written.  No gradients, as kv_append."""
+    head_dim), in out if given.  scale defaults to head_dim ** -0.5.  With a
+    tree (:class:`KVTree`) a new token sees its chain of parents only, instead
+    of all new tokens before it.  Rows of no sequence are not written.  No
+    gradients, as kv_append."""
     torch = _torch or _need_torch()
     dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, q.dtype
     same = batch.dev == dev and q.get_device() == dev
@@ -535,6 +613,10 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
     if prefix is not None:
         _int32("attn: prefix", prefix, batch.n_seqs)
         same = same and prefix.get_device() == dev
+    if tree is not None:
+        if tree.n_tokens != N:
+            _refuse(QMM_ERR_SHAPE, "attn: the tree has to be of the batch's tokens")
+        same = same and tree.dev == dev
     if not same:
         _refuse(QMM_ERR_UNSUPPORTED, "attn: tensors have to lie on one GPU, and out be of q's type")
     if not 0 <= window < 1 << 31 or not 0 <= algo <= 2:  # ctypes would take their low 32 bits
@@ -546,18 +628,148 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
     if stream is not None or torch.cuda.current_device() != dev:
         handle, where = _elsewhere(dev, stream)
         with where:
-            return _attend(cache, batch, opts, xtype, q, ldq, n_q, out, handle)
-    return _attend(cache, batch, opts, xtype, q, ldq, n_q, out, _raw_stream(dev))
+            return _attend(cache, batch, tree, opts, xtype, q, ldq, n_q, out, handle)
+    return _attend(cache, batch, tree, opts, xtype, q, ldq, n_q, out, _raw_stream(dev))
 
 
-def _attend(cache, batch, opts, xtype, q, ldq, n_q, out, handle):
+def _attend(cache, batch, tree, opts, xtype, q, ldq, n_q, out, handle):
     L = lib()
-    need = L.qmm_attn_work(cache.ref, batch.ref, opts, xtype, n_q)
+    need = (L.qmm_attn_work if tree is None else L.qmm_attn_tree_work)(cache.ref, batch.ref, opts, xtype, n_q)
     if out is None:
         out = _new_out(q)
     work = _torch.empty(need, dtype=_torch.uint8, device=q.device) if need else None
-    rc = L.qmm_attn(cache.ref, batch.ref, opts, xtype, q.data_ptr(), ldq, n_q, out.data_ptr(), _ptr(work), need,
-                    handle)
+    if tree is None:
+        rc = L.qmm_attn(cache.ref, batch.ref, opts, xtype, q.data_ptr(), ldq, n_q, out.data_ptr(), _ptr(work), need,
+                        handle)
+    else:
+        rc = L.qmm_attn_tree(cache.ref, batch.ref, tree.ref, opts, xtype, q.data_ptr(), ldq, n_q, out.data_ptr(),
+                             _ptr(work), need, handle)
     if rc != QMM_OK:
-        raise QmmError(rc, "qmm_attn")
+        raise QmmError(rc, "qmm_attn" if tree is None else "qmm_attn_tree")
     return out
+
+
+class KVLayers:
+    """The caches of a model's layers, of one geometry and on one GPU, for what
+    moves rows in all of them at once."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not 0 < len(self.caches) <= 4096:
+            _refuse(QMM_ERR_SHAPE, "KVLayers: 1 to 4096 caches")
+        f = self.caches[0]
+        if any((c.type, c.n_kv, c.head_dim, c.page_size, c.n_pages) != (f.type, f.n_kv, f.head_dim, f.page_size, f.n_pages)
+               for c in self.caches):
+            _refuse(QMM_ERR_SHAPE, "KVLayers: the caches have to be of one geometry")
+        if any(c.dev != f.dev for c in self.caches):
+            _refuse(QMM_ERR_UNSUPPORTED, "KVLayers: the caches have to lie on one GPU")
+        self.dev, self.n = f.dev, len(self.caches)
+        self.c = (qmm_kv_cache * self.n)(*[c.c for c in self.caches])
+
+
+def _on(dev: int, stream):
+    """(stream handle, context or None) for a call on tensors of device dev."""
+    if stream is not None or _need_torch().cuda.current_device() != dev:
+        return _elsewhere(dev, stream)
+    return _raw_stream(dev), None
+
+
+def kv_copy(layers: KVLayers, src, dst, rows=None, stream=None):
+    """Copies the pages src to dst (int32, as many of each) in every layer: the
+    first rows[i] tokens of each, or all.  No page in dst twice, or in src and
+    dst of different pairs."""
+    n = src.numel()
+    _int32("kv_copy: src", src, n)
+    _int32("kv_copy: dst", dst, n)
+    if rows is not None:
+        _int32("kv_copy: rows", rows, n)
+    if _device_of("kv_copy", src, dst, rows) != layers.dev:
+        _refuse(QMM_ERR_UNSUPPORTED, "kv_copy: tensors have to lie on the layers' GPU")
+    if not n:
+        return
+    handle, where = _on(layers.dev, stream)
+    L, args = lib(), (layers.c, layers.n, src.data_ptr(), dst.data_ptr(), _ptr(rows), n, handle)
+    if where is None:
+        rc = L.qmm_kv_copy(*args)
+    else:
+        with where:
+            rc = L.qmm_kv_copy(*args)
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_copy")
+
+
+def kv_compact(layers: KVLayers, table, first, keep, n_keep, kv_len=None, stream=None):
+    """Moves the tokens keep[s, :n_keep[s]] (int32, rising) of every sequence to
+    its indexes from first[s] on, in place in every layer, and writes the new
+    lengths first + n_keep to kv_len if given."""
+    if table.dim() != 2 or keep.dim() != 2:
+        _refuse(QMM_ERR_SHAPE, "kv_compact: table and keep have to be n_seqs x width")
+    n, width = keep.shape
+    _int32("kv_compact: table", table, n, table.shape[1])
+    _int32("kv_compact: first", first, n)
+    _int32("kv_compact: keep", keep, n, width)
+    _int32("kv_compact: n_keep", n_keep, n)
+    if kv_len is not None:
+        _int32("kv_compact: kv_len", kv_len, n)
+    if _device_of("kv_compact", table, first, keep, n_keep, kv_len) != layers.dev:
+        _refuse(QMM_ERR_UNSUPPORTED, "kv_compact: tensors have to lie on the layers' GPU")
+    handle, where = _on(layers.dev, stream)
+    L, args = lib(), (layers.c, layers.n, table.data_ptr(), n, table.shape[1], first.data_ptr(), keep.data_ptr(),
+                      n_keep.data_ptr(), width, _ptr(kv_len), handle)
+    if where is None:
+        rc = L.qmm_kv_compact(*args)
+    else:
+        with where:
+            rc = L.qmm_kv_compact(*args)
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_compact")
+
+
+# ------------------------------------------------------------- the logits
+
+LogProbs = collections.namedtuple("LogProbs", "tokens entropy top_ids top")
+
+
+def logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, softcap: float = 0.0, stream=None) -> LogProbs:
+    """What rows of logits (rows, vocab; float32 or bfloat16, rows may be apart)
+    say of tokens: the log probabilities of tokens (int32, rows x any), the
+    entropy of each row, and the top largest logits' ids and log probabilities
+    (64 at most).  x = scale * softcap * tanh(logits / softcap).  What is not
+    asked for is None.  No gradients: logits that require them are refused
+    where torch records them."""
+    torch = _torch or _need_torch()
+    if logits.dim() != 2:
+        _refuse(QMM_ERR_SHAPE, "logprobs: logits have to be rows x vocab")
+    rows, vocab = logits.shape
+    xtype = _xtype("logprobs", logits.dtype)
+    if not 0 <= top <= 64:
+        _refuse(QMM_ERR_SHAPE, "logprobs: top has to be 0 to 64")
+    if vocab > 1 and logits.stride(1) != 1:
+        _refuse(QMM_ERR_UNSUPPORTED, "logprobs: the values of a row have to lie one after another")
+    ld = logits.stride(0) if rows > 1 else vocab
+    if tokens is not None:
+        if tokens.dim() != 2:
+            _refuse(QMM_ERR_SHAPE, "logprobs: tokens have to be rows x any")
+        _int32("logprobs: tokens", tokens, rows, tokens.shape[1])
+    dev = _device_of("logprobs", logits, tokens)
+    _no_grad("logprobs", logits)
+    handle, where = _on(dev, stream)
+    if where is None:
+        return _logprobs(logits, xtype, ld, rows, vocab, tokens, top, scale, softcap, handle)
+    with where:
+        return _logprobs(logits, xtype, ld, rows, vocab, tokens, top, scale, softcap, handle)
+
+
+def _logprobs(logits, xtype, ld, rows, vocab, tokens, top, scale, softcap, handle):
+    L, given = lib(), 0 if tokens is None else tokens.shape[1]
+    new = logits.new_empty
+    need = L.qmm_logprobs_work(xtype, rows, vocab, top)
+    logp = new((rows, given), dtype=_torch.float32) if tokens is not None else None
+    entropy = new(rows, dtype=_torch.float32)
+    ids, best = (new((rows, top), dtype=_torch.int32), new((rows, top), dtype=_torch.float32)) if top else (None, None)
+    work = new(need, dtype=_torch.uint8) if need else None
+    rc = L.qmm_logprobs(xtype, logits.data_ptr(), ld, rows, vocab, scale, softcap, _ptr(tokens), given, _ptr(logp),
+                        entropy.data_ptr(), top, _ptr(ids), _ptr(best), _ptr(work), need, handle)
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_logprobs")
+    return LogProbs(logp, entropy, ids, best)

@@ -125,6 +125,7 @@ struct TileAt {
     int s, first, tokens, row;  // row: of the inputs, of token `first`
     int pos, len, pre;          // index of the first token, readable keys, prefix
     int end, low;               // keys any of the tokens sees: [low, end) and [0, pre)
+    int base, n, kv;            // index of the sequence's first new token, new tokens, and cached ones with them
 };
 
 // What a lane reads of its sequence (nothing of it is trusted further than
@@ -142,7 +143,9 @@ __device__ __forceinline__ SeqAt seq_at(const AttnArgs& a, int s) {
     return q;
 }
 
-// The row tile that begins with token `first` of sequence s.
+// The row tile that begins with token `first` of sequence s.  In a tree any new
+// token may be seen, and positions begin with the first new token's.
+template <bool TREE>
 __device__ __forceinline__ TileAt tile_at(const AttnArgs& a, int s, const SeqAt& q, int first) {
     TileAt t;
     t.s = s;
@@ -153,9 +156,41 @@ __device__ __forceinline__ TileAt tile_at(const AttnArgs& a, int s, const SeqAt&
     t.len = (int64_t)q.kv < room ? q.kv : (int)room;
     t.pos = q.kv - (q.q1 - q.q0) + first;
     t.pre = q.pre;
-    t.end = max(0, min(t.len, t.pos + t.tokens));
-    t.low = a.window > 0 && t.pos >= a.window ? t.pos - a.window + 1 : 0;
+    t.n = q.q1 - q.q0;
+    t.kv = q.kv;
+    t.base = q.kv - t.n;
+    t.end = TREE ? t.len : max(0, min(t.len, t.pos + t.tokens));
+    const int from = TREE ? t.base : t.pos;
+    t.low = a.window > 0 && from >= a.window ? from - a.window + 1 : 0;
     return t;
+}
+
+// A row of a tree: its position, and what it sees of the new tokens.
+struct TreeRow {
+    const uint64_t* seen;
+    const int32_t* depth;  // of the sequence's first new token
+    int pos;
+};
+__device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const TileAt& t, int mt) {
+    const int64_t row = t.row + mt;
+    const int32_t d = a.depth[row];
+    // (no depth is trusted further than that it is a number: positions stay below 2^31)
+    return TreeRow{a.tree + row * a.words, a.depth + (t.row - t.first), t.base + min(max(d, 0), t.n)};
+}
+// Which of the keys kb .. kb + 63 the row sees, window and prefix apart: those
+// before the new tokens, and its own of these.
+__device__ __forceinline__ uint64_t tree_bits(const AttnArgs& a, const TileAt& t, const TreeRow& r, int kb) {
+    const int64_t off = (int64_t)kb - t.base;
+    const int64_t w = off >> 6;
+    const int sh = (int)(off & 63);
+    const uint64_t lo = w >= 0 && w < a.words ? r.seen[w] : 0, hi = w >= -1 && w + 1 < a.words ? r.seen[w + 1] : 0;
+    const uint64_t before = off >= 0 ? 0 : off <= -64 ? ~uint64_t(0) : (uint64_t(1) << -off) - 1;
+    return before | lo >> sh | (sh ? hi << (64 - sh) : 0);
+}
+// The position of key j.
+__device__ __forceinline__ int tree_place(const TileAt& t, const TreeRow& r, int j) {
+    const int i = j - t.base;  // (j is below 2^30, the base above -2^23)
+    return i < 0 || i >= t.n ? j : t.base + min(max(r.depth[i], 0), t.n);
 }
 
 // A work item: a row tile of a sequence, and a part of the keys it sees.
@@ -173,6 +208,7 @@ struct Work {
 // (64 conversations of 8k to 16k keys: 382 -> 338 us against as many splits
 // of each).  Without splits (0) a row tile is one item.  Items go split by
 // split within a sequence; `last_first` turns the row tiles around.
+template <bool TREE>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, bool last_first = false) {
     const int lane = threadIdx.x & 63, n = a.c.n_seqs;
     SeqAt q = {};
@@ -183,7 +219,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
         q = seq_at(a, s);
         if (q.q1 <= q.q0) return;
         tiles = ((q.q1 - q.q0 - 1) >> a.tile_shift) + 1;
-        const TileAt t = tile_at(a, s, q, 0);
+        const TileAt t = tile_at<TREE>(a, s, q, 0);
         const int pre = (t.pre + 31) >> 5;
         keys = pre + max(0, ((t.len + 31) >> 5) - max(pre, t.low >> 5));
     };
@@ -226,7 +262,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
             if (last_first) tile = t - 1 - tile;
             const SeqAt u = {__builtin_amdgcn_readlane(q.q0, at), __builtin_amdgcn_readlane(q.q1, at),
                              __builtin_amdgcn_readlane(q.kv, at), __builtin_amdgcn_readlane(q.pre, at)};
-            w.at = tile_at(a, s0 + at, u, tile << a.tile_shift);
+            w.at = tile_at<TREE>(a, s0 + at, u, tile << a.tile_shift);
             return true;
         }
         base += __builtin_amdgcn_readlane(upto, 63);

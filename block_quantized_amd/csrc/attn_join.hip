@@ -118,11 +118,16 @@ hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStrea
     }
 }
 
+template <int CT, bool TREE>
+static hipError_t attn_typed(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+    if (algo != 2) return launch_attn_split_of<CT, TREE>(head_dim, xtype, a, s);
+    return head_dim <= 128 ? launch_attn_tile_narrow<CT, TREE>(head_dim, xtype, a, s)
+                           : launch_attn_tile_wide<CT, TREE>(head_dim, xtype, a, s);
+}
+
 template <int CT>
 static hipError_t attn_of(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    if (algo != 2) return launch_attn_split_of<CT>(head_dim, xtype, a, s);
-    return head_dim <= 128 ? launch_attn_tile_narrow<CT>(head_dim, xtype, a, s)
-                           : launch_attn_tile_wide<CT>(head_dim, xtype, a, s);
+    return a.tree ? attn_typed<CT, true>(algo, head_dim, xtype, a, s) : attn_typed<CT, false>(algo, head_dim, xtype, a, s);
 }
 
 hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {

@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t ld16(const uint8_t* p) { return *reinterpret
 template <int NB>
 constexpr int kStage = 32 * 34 * NB + 64 * NB;
 
-template <int CT, int NB, bool XB>
+template <int CT, int NB, bool XB, bool TREE>
 __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     // the parts of P, and those of Q, with the MFMAs that take them
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     u4v(*s_q)[QP][64] = reinterpret_cast<u4v(*)[QP][64]>(smem);
     const int groups = a.c.n_kv * a.chunks, item = (int)(blockIdx.x / groups), hb = blockIdx.x % groups;
     Work w;
-    if (!find_work(a, item, w)) return;
+    if (!find_work<TREE>(a, item, w)) return;
     const TileAt at = w.at;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -75,7 +75,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     // row m of the tile: token m / heads, head m % heads
     const int rows = min(16, at.tokens * heads);
     const int mr = min(m, rows - 1), mt = mr / heads, head = head0 + mr % heads;
-    const int p_row = at.pos + mt;
+    TreeRow tree = {};
+    if constexpr (TREE) tree = tree_row(a, at, mt);
+    const int p_row = TREE ? tree.pos : at.pos + mt;
 
     // ---- the tiles of this split
     const int n_pre = (at.pre + 31) >> 5;
@@ -84,7 +86,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     const int per = (n_tiles + w.splits - 1) / w.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
     // every row sees keys from here (no index less a window passes 32 bits from 0 on; rows below it see none)
-    const int low_last = a.window > 0 ? max(at.pos + at.tokens, 0) - a.window : INT32_MIN;
+    const int low_last = a.window > 0 ? max(TREE ? at.kv : at.pos + at.tokens, 0) - a.window : INT32_MIN;
+    // and up to here
+    const int all_see = TREE ? at.base : at.pos + 1;
 
     // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
     // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page
@@ -111,7 +115,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
         kb = 32 * (t < n_pre ? t : t - n_pre + w0);
         whole = r0[0] >= 0 && r0[1] >= 0 &&
-                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, at.pos + 1)));
+                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, all_see)));
     };
     // the first lookup is under way while the queries are prepared
     int t = t0 + wave;
@@ -186,10 +190,23 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
             for (int i = 0; i < 8; ++i) sc[i] = kept(i >> 2, kb + 16 * (i >> 2) + 4 * g + (i & 3)) ? sc[i] : 0.f;
         }
         if (a.softcap > 0.f) cap_scores(sc, 1.0f, a.softcap);
+        int place[8];
+        uint64_t bits = 0;
+        if constexpr (TREE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) place[i] = kb + 16 * (i >> 2) + 4 * g + (i & 3);
+            if (!whole) {
+                bits = tree_bits(a, at, tree, kb) >> (4 * g);
+                if (a.slopes || a.window > 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) place[i] = tree_place(at, tree, place[i]);
+                }
+            }
+        }
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sc[i] -= slope * fabsf((float)(p_row - (kb + 16 * (i >> 2) + 4 * g + (i & 3))));
+                sc[i] -= slope * fabsf((float)(p_row - (TREE ? place[i] : kb + 16 * (i >> 2) + 4 * g + (i & 3))));
         }
         if (!whole) {
 #pragma unroll
@@ -197,8 +214,9 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                 const int u = i >> 2, key = kb + 16 * u + 4 * g + (i & 3);
                 // (without branches: ROCm 7.2's compiler keeps sc as one tuple of registers, and where the assignment
                 // stood in nested branches it copied the tuple as it was before over it, with and without honoured NaNs)
-                const bool seen =
-                    (key < at.len) & (r0[u] >= 0) & (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
+                const bool near = TREE ? (bits >> (16 * u + (i & 3)) & 1) & (p_row - place[i] < reach)
+                                       : (key <= p_row) & (p_row - key < reach);
+                const bool seen = (key < at.len) & (r0[u] >= 0) & (near | (key < at.pre));
                 sc[i] = seen ? sc[i] : -INFINITY;
             }
         }
@@ -484,29 +502,29 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     }
 }
 
-template <int CT, int NB, bool XB>
+template <int CT, int NB, bool XB, bool TREE>
 hipError_t split_typed(const AttnArgs& a, hipStream_t s) {
     const int64_t grid = a.items * a.c.n_kv * a.chunks;  // below 2^32 work-items
-    hipError_t e = launch(attn_split_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipError_t e = launch(attn_split_kernel<CT, NB, XB, TREE>, dim3((unsigned)grid), dim3(256), 0, s, a);
     if (e != hipSuccess || !a.splits) return e;
     return launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 
-template <int CT, int NB>
+template <int CT, int NB, bool TREE>
 hipError_t split_x(int xtype, const AttnArgs& a, hipStream_t s) {
-    return xtype == QMM_BF16 ? split_typed<CT, NB, true>(a, s) : split_typed<CT, NB, false>(a, s);
+    return xtype == QMM_BF16 ? split_typed<CT, NB, true, TREE>(a, s) : split_typed<CT, NB, false, TREE>(a, s);
 }
 
 }  // namespace
 
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_split_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
-    case 64: return split_x<CT, 2>(xtype, a, s);
-    case 96: return split_x<CT, 3>(xtype, a, s);
-    case 128: return split_x<CT, 4>(xtype, a, s);
-    case 192: return split_x<CT, 6>(xtype, a, s);
-    case 256: return split_x<CT, 8>(xtype, a, s);
+    case 64: return split_x<CT, 2, TREE>(xtype, a, s);
+    case 96: return split_x<CT, 3, TREE>(xtype, a, s);
+    case 128: return split_x<CT, 4, TREE>(xtype, a, s);
+    case 192: return split_x<CT, 6, TREE>(xtype, a, s);
+    case 256: return split_x<CT, 8, TREE>(xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -3,5 +3,5 @@
 #include "attn_split.h"
 
 namespace qmm {
-template hipError_t launch_attn_split_of<QMM_BF16>(int, int, const AttnArgs&, hipStream_t);
+template hipError_t launch_attn_split_of<QMM_BF16, false>(int, int, const AttnArgs&, hipStream_t);
 }

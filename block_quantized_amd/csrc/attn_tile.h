@@ -106,7 +106,7 @@ constexpr int q_parts(int ct, bool xb) { return xb ? 1 : ct == QMM_BF16 ? 3 : 2;
 constexpr int p_parts(int ct, bool xb) { return xb ? 2 : q_parts(ct, xb); }
 constexpr int wave_rows(int ct, int nb, bool xb) { return nb > 4 || q_parts(ct, xb) == 3 ? 16 : 32; }
 
-template <int CT, int NB, bool XB>
+template <int CT, int NB, bool XB, bool TREE>
 __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void attn_tile_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     // head's keys and values.
     const int groups = a.c.n_kv * a.chunks, item = (int)(blockIdx.x / groups), hb = blockIdx.x % groups;
     Work w;
-    if (!find_work(a, item, w, true)) return;
+    if (!find_work<TREE>(a, item, w, true)) return;
     const TileAt at = w.at;
     const int lane = threadIdx.x & 63, r = lane % R, h = lane / R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -145,9 +145,13 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     const int heads = min(a.chunk, kvh * G + G - head0);
     const int rows = at.tokens * heads;
     const int mr = min(R * wave + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
-    const int p_row = at.pos + mt;
-    // the positions of the wave's first and last row
-    const int p_first = at.pos + min(R * wave, rows - 1) / heads, p_last = at.pos + min(R * wave + R - 1, rows - 1) / heads;
+    TreeRow tree = {};
+    if constexpr (TREE) tree = tree_row(a, at, mt);
+    const int p_row = TREE ? tree.pos : at.pos + mt;
+    // the positions of the wave's first and last row (in a tree, of any)
+    const int p_first = TREE ? at.base : at.pos + min(R * wave, rows - 1) / heads;
+    const int p_last = TREE ? at.kv - 1 : at.pos + min(R * wave + R - 1, rows - 1) / heads;
+    const int all_see = TREE ? at.base : p_first + 1;  // every row of the wave sees the keys up to here
     const bool idle = R * wave >= rows;
     // the key, in its tile, of value i of the lane's scores
     auto key_of = [&](int i) {
@@ -461,20 +465,24 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             cap_scores(s, f, a.softcap);
             f = 1.0f;
         }
+        const bool whole = page[0] && page[1] && page[2] && page[3] &&
+                           ((kb + kKeys <= at.pre) || (kb >= low_last && kb + kKeys <= min(at.len, all_see)));
+        auto place = [&](int key) { return TREE && kb + kKeys > at.base ? tree_place(at, tree, key) : key; };
         if (a.slopes) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) s[i] = s[i] * f - slope * fabsf((float)(p_row - (kb + key_of(i))));
+            for (int i = 0; i < R; ++i) s[i] = s[i] * f - slope * fabsf((float)(p_row - place(kb + key_of(i))));
             f = 1.0f;
         }
-        const bool whole = page[0] && page[1] && page[2] && page[3] &&
-                           ((kb + kKeys <= at.pre) || (kb >= low_last && kb + kKeys <= min(at.len, p_first + 1)));
         if (!whole) {
+            const uint64_t bits = TREE ? tree_bits(a, at, tree, kb) >> (R == 32 ? 4 * h : 8 * h) : 0;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int key = kb + key_of(i);
                 const bool paged = R == 32 ? page[i >> 3] : (h >> 1 ? page[2 * (i >> 3) + 1] : page[2 * (i >> 3)]);
-                const bool seen =
-                    paged & (key < at.len) & (((key <= p_row) & (p_row - key < reach)) | (key < at.pre));
+                const bool near = TREE ? (bits >> (key_of(i) - (R == 32 ? 4 * h : 8 * h)) & 1) &
+                                             (a.window <= 0 || p_row - place(key) < reach)
+                                       : (key <= p_row) & (p_row - key < reach);
+                const bool seen = paged & (key < at.len) & (near | (key < at.pre));
                 s[i] = seen ? s[i] : -INFINITY;
             }
         }
@@ -625,38 +633,38 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
 }
 
-template <int CT, int NB, bool XB>
+template <int CT, int NB, bool XB, bool TREE>
 hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
     const int64_t grid = a.items * a.c.n_kv * a.chunks;  // below 2^32 work-items
-    hipError_t e = launch(attn_tile_kernel<CT, NB, XB>, dim3((unsigned)grid), dim3(64 * kTileRows / wave_rows(CT, NB, XB)), 0,
+    hipError_t e = launch(attn_tile_kernel<CT, NB, XB, TREE>, dim3((unsigned)grid), dim3(64 * kTileRows / wave_rows(CT, NB, XB)), 0,
                           s, a);
     return e != hipSuccess || !a.splits ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 
-template <int CT, int NB>
+template <int CT, int NB, bool TREE>
 hipError_t tile_x(int xtype, const AttnArgs& a, hipStream_t s) {
-    return xtype == QMM_BF16 ? tile_typed<CT, NB, true>(a, s) : tile_typed<CT, NB, false>(a, s);
+    return xtype == QMM_BF16 ? tile_typed<CT, NB, true, TREE>(a, s) : tile_typed<CT, NB, false, TREE>(a, s);
 }
 
 }  // namespace
 
 // Heads of up to 128 values, and wider ones: units of their own, so that they
 // compile side by side.
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
-    case 64: return tile_x<CT, 2>(xtype, a, s);
-    case 96: return tile_x<CT, 3>(xtype, a, s);
-    case 128: return tile_x<CT, 4>(xtype, a, s);
+    case 64: return tile_x<CT, 2, TREE>(xtype, a, s);
+    case 96: return tile_x<CT, 3, TREE>(xtype, a, s);
+    case 128: return tile_x<CT, 4, TREE>(xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }
 
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_tile_wide(int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (head_dim) {
-    case 192: return tile_x<CT, 6>(xtype, a, s);
-    case 256: return tile_x<CT, 8>(xtype, a, s);
+    case 192: return tile_x<CT, 6, TREE>(xtype, a, s);
+    case 256: return tile_x<CT, 8, TREE>(xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }

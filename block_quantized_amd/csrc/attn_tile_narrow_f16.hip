@@ -2,5 +2,5 @@
 #include "attn_tile.h"
 
 namespace qmm {
-template hipError_t launch_attn_tile_narrow<QMM_F16>(int, int, const AttnArgs&, hipStream_t);
+template hipError_t launch_attn_tile_narrow<QMM_F16, false>(int, int, const AttnArgs&, hipStream_t);
 }

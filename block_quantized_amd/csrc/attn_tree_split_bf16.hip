@@ -1,0 +1,6 @@
+// attn_tree_split_bf16.hip — the split kernels for trees of new tokens over BF16 caches.
+#include "attn_split.h"
+
+namespace qmm {
+template hipError_t launch_attn_split_of<QMM_BF16, true>(int, int, const AttnArgs&, hipStream_t);
+}

@@ -1,0 +1,6 @@
+// attn_tree_tile_wide_bf16.hip — the wide tile kernels for trees of new tokens over BF16 caches.
+#include "attn_tile.h"
+
+namespace qmm {
+template hipError_t launch_attn_tile_wide<QMM_BF16, true>(int, int, const AttnArgs&, hipStream_t);
+}

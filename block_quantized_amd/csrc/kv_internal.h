@@ -53,6 +53,49 @@ struct AttnArgs {
     int64_t items;       // work items of a head at most
     int32_t slots;       // rows of an item at most: tokens of a row tile x chunk
     int64_t parts;       // rows of the workspace: items x row tiles of heads x slots
+    // a tree of new tokens (tree kernels only): who sees whom, and depths
+    const uint64_t* tree;
+    const int32_t* depth;
+    int32_t words;
+};
+
+// What builds a tree from its tokens' parents.
+struct TreeArgs {
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* parents;
+    uint64_t* seen;
+    int32_t* depth;
+    int32_t* pos;  // nullptr: not wanted
+    int64_t n_tokens;
+    int32_t n_seqs, words;
+};
+
+// Words of 64 new tokens that a row of a tree has at most.
+constexpr int kTreeWords = 16;
+
+// The layers of a model, as many as a launch takes.
+constexpr int kMaxLayers = 64;
+struct LayerArgs {
+    uint8_t* pool[2 * kMaxLayers];  // k and v of each
+};
+
+struct CopyArgs {
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* rows;  // nullptr: whole pages
+    int64_t n, n_pages, page_bytes;
+    int32_t n_kv, page_size, row_bytes;
+};
+
+struct CompactArgs {
+    const int32_t* table;
+    const int32_t* first;
+    const int32_t* keep;
+    const int32_t* n_keep;
+    int32_t* kv_len;  // nullptr: not wanted
+    int64_t n_pages;
+    int32_t n_seqs, table_width, page_size, n_kv, width;
 };
 
 // Rows of a row tile: of the split and of the tile kernels.
@@ -77,15 +120,18 @@ __device__ __forceinline__ int find_seq(const KvArgs& c, int row, int count) {
 
 hipError_t launch_rope_freqs(double* freqs, int n_rot, double base, double scale, const float* factors, hipStream_t s);
 hipError_t launch_kv_append(int type, int head_dim, int xtype, const AppendArgs& a, hipStream_t s);
-// Attention by the split (1) or the tile (2) kernels; each unit of a cache
-// type instantiates its own.
+// Attention by the split (1) or the tile (2) kernels, of a tree of new tokens
+// where a.tree is given; each unit of a cache type instantiates its own.
 hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_split_of(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
-template <int CT>
+template <int CT, bool TREE>
 hipError_t launch_attn_tile_wide(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+hipError_t launch_kv_tree(const TreeArgs& a, hipStream_t s);
+hipError_t launch_kv_copy(int layers, const LayerArgs& l, const CopyArgs& a, hipStream_t s);
+hipError_t launch_kv_compact(int type, int head_dim, int layers, const LayerArgs& l, const CompactArgs& a, hipStream_t s);
 hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 
 }  // namespace qmm

@@ -170,6 +170,84 @@ size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const
  * may be another. */
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q);
 
+/* ---- checking drafted tokens
+ *
+ * A step may carry several drafted tokens a sequence that are not one text but
+ * a tree: each goes on from an earlier one of them, its parent, or from the
+ * cached tokens.  The new tokens are appended in any order in which parents
+ * come first (qmm_kv_append with pos), attend only to what they go on from
+ * (qmm_attn_tree), and afterwards the rows of the path that is kept move
+ * together (qmm_kv_compact). */
+
+/* Who sees whom among the new tokens of a batch.  Row r of the batch, token i of
+ * its sequence's n new ones, sees the sequence's new token j where bit j % 64 of
+ * seen[r * words + j / 64] is set; new tokens from 64 * words on are seen by
+ * none.  It stands at position kv_len - n + depth[r]. */
+typedef struct {
+    uint64_t* seen;  /* device, n_tokens x words, 16-byte aligned        */
+    int32_t* depth;  /* device, n_tokens                                 */
+    int32_t words;   /* 1 .. 16: room for 64 * words new tokens of a
+                        sequence                                         */
+} qmm_kv_tree;
+
+/* Fills a tree from the parents of its tokens: a token sees its chain of
+ * parents and itself, and its depth is the number of its parents.
+ *   batch   : q_start, kv_len, n_seqs and n_tokens count
+ *   parents : device, n_tokens: the parent's place among the sequence's new
+ *             tokens, which has to be before the token's; anything else (-1)
+ *             is no parent
+ *   pos     : device, n_tokens, written with positions for qmm_rope; or NULL
+ * Tokens of a sequence from 64 * words on are no part of the tree: they see
+ * none of the new tokens, not themselves either, at depth 0.  Rows of no
+ * sequence are not written. */
+int qmm_kv_tree_build(const qmm_kv_batch* batch, const int32_t* parents, const qmm_kv_tree* tree, int32_t* pos,
+                      void* stream);
+
+/* qmm_attn for a tree of new tokens: with p = kv_len - n + depth[r] the row's
+ * position and p_j that of key j (its index, or for a new token kv_len - n +
+ * depth of its row), scores go through the same steps with |p - p_j| for the
+ * slopes, and key j < kv_len is visible if
+ *   ((j < kv_len - n or the row sees that new token)
+ *    and (window == 0 or p - p_j < window))  or  j < prefix[s].
+ * Keys and values of all new tokens have to be finite.  Everything else is as
+ * in qmm_attn, the workspace (qmm_attn_tree_work) too.  No read leaves the
+ * buffers for any contents of the tree. */
+int qmm_attn_tree(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_kv_tree* tree, const qmm_attn_opts* opts,
+                  int xtype, const void* q, int64_t ldq, int n_q, void* out, void* work, size_t work_bytes, void* stream);
+
+/* Bytes of workspace that qmm_attn_tree needs; as qmm_attn_work. */
+size_t qmm_attn_tree_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
+                          int n_q);
+
+/* Copies rows of pages, in the layers of a model at once: what a conversation
+ * that goes on in two ways needs of the page they would both write to.
+ *   caches : host array of count layers of the same geometry
+ *   src, dst : device, n page numbers each; a pair with one outside [0, n_pages)
+ *            is left out
+ *   rows   : device, n: tokens of the page that are copied (held to [0,
+ *            page_size]); NULL: all.  What lies behind stays as it is
+ * No page may be in dst twice, or in src and dst of different pairs. */
+int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const int32_t* dst, const int32_t* rows,
+                int64_t n, void* stream);
+
+/* Moves the rows that sequences keep to consecutive indexes, in place, in the
+ * layers of a model at once: sequence s's token keep[s * width + i] goes to index
+ * first[s] + i, for i < n_keep[s].  The rest of the cache stays as it is.
+ *   caches : host array of count layers of the same geometry
+ *   table  : device, n_seqs x table_width pages, as in qmm_kv_batch
+ *   first  : device, n_seqs
+ *   keep   : device, n_seqs x width: rising in each sequence, so that
+ *            keep[s][i] >= first[s] + i
+ *   n_keep : device, n_seqs (held to [0, width])
+ *   kv_len : device, n_seqs, written with first[s] + n_keep[s]; or NULL.  None of
+ *            the inputs
+ * A token whose old or new place has no page is not moved.  Where keep does not
+ * rise, what moves is undefined, but stays within the cache.  The rows that are
+ * written must not lie in pages of other sequences too. */
+int qmm_kv_compact(const qmm_kv_cache* caches, int count, const int32_t* table, int n_seqs, int table_width,
+                   const int32_t* first, const int32_t* keep, const int32_t* n_keep, int width, int32_t* kv_len,
+                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
