@@ -30,8 +30,11 @@ UNITS = {
     "probe.hip": [],
     # stored cache rows are defined to the bit, as the codec's blocks are
     "kv_append.hip": ["-ffp-contract=off"],
-    **{f"attn_{tree}{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-       for tree in ("", "tree_") for kind in ("split", "tile_narrow", "tile_wide") for cache in ("q8_0", "f16", "bf16")},
+    **{f"attn_{kind}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+       for kind in ("split", "tile_narrow", "tile_wide", "tree_split") for cache in ("q8_0", "f16", "bf16")},
+    **{f"attn_tree_tile_{heads}_{cache}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+       for heads in ("narrow", "wide") for cache in ("f16", "bf16")},
+    "attn_tree_q8_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_join.hip": [],
     "kv_tree.hip": [],
     "kv_move.hip": [],

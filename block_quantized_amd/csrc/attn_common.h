@@ -79,6 +79,22 @@ __device__ __forceinline__ u4v codes8_f16(uint2 w) {
                codes_f16(hi, 0x04030402u)};
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+// Two fp16 parts of d c / 128 for pairs of int8 codes c and scales d: the product
+// rounded, and what that leaves off, which has no more bits than fp16 holds, so
+// that the parts are exact above its smallest step.  The codes lie in the low
+// bytes of 16 bits each (0x4800 | u is 8 + u / 128; with u = c + 128 9 less is c / 128).
+__device__ __forceinline__ void scaled_codes(uint32_t bytes, half2v d, uint32_t (&part)[2]) {
+    const half2v nine = {(_Float16)9.0f, (_Float16)9.0f};
+    const half2v c = __builtin_bit_cast(half2v, bytes ^ 0x48804880u) - nine, hi = c * d;
+    part[0] = __builtin_bit_cast(uint32_t, hi);
+    part[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, d, -hi));
+}
+
 // The running maximum of a row is raised when a score (times log2 e) passes it by
 // this: weights reach 2^kSlack, which spares the cross-lane maximum and the
 // rescaling for almost every tile.

@@ -118,23 +118,29 @@ hipError_t launch_attn_join(int head_dim, int xtype, const AttnArgs& a, hipStrea
     }
 }
 
-template <int CT, bool TREE>
-static hipError_t attn_typed(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    if (algo != 2) return launch_attn_split_of<CT, TREE>(head_dim, xtype, a, s);
-    return head_dim <= 128 ? launch_attn_tile_narrow<CT, TREE>(head_dim, xtype, a, s)
-                           : launch_attn_tile_wide<CT, TREE>(head_dim, xtype, a, s);
-}
-
 template <int CT>
 static hipError_t attn_of(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
-    return a.tree ? attn_typed<CT, true>(algo, head_dim, xtype, a, s) : attn_typed<CT, false>(algo, head_dim, xtype, a, s);
+    if (algo != 2) return launch_attn_split_of<CT, false>(head_dim, xtype, a, s);
+    return head_dim <= 128 ? launch_attn_tile_narrow<CT, false>(head_dim, xtype, a, s)
+                           : launch_attn_tile_wide<CT, false>(head_dim, xtype, a, s);
+}
+
+// The same for trees of new tokens.  Q8_0 rows have kernels of their own instead of the tile kernels.
+template <int CT>
+static hipError_t tree_of(int algo, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
+    if (algo != 2) return launch_attn_split_of<CT, true>(head_dim, xtype, a, s);
+    if constexpr (CT == QMM_Q8_0)
+        return launch_attn_tree_q8_0(head_dim, xtype, a, s);
+    else
+        return head_dim <= 128 ? launch_attn_tile_narrow<CT, true>(head_dim, xtype, a, s)
+                               : launch_attn_tile_wide<CT, true>(head_dim, xtype, a, s);
 }
 
 hipError_t launch_attn(int algo, int type, int head_dim, int xtype, const AttnArgs& a, hipStream_t s) {
     switch (type) {
-    case QMM_Q8_0: return attn_of<QMM_Q8_0>(algo, head_dim, xtype, a, s);
-    case QMM_F16: return attn_of<QMM_F16>(algo, head_dim, xtype, a, s);
-    case QMM_BF16: return attn_of<QMM_BF16>(algo, head_dim, xtype, a, s);
+    case QMM_Q8_0: return a.tree ? tree_of<QMM_Q8_0>(algo, head_dim, xtype, a, s) : attn_of<QMM_Q8_0>(algo, head_dim, xtype, a, s);
+    case QMM_F16: return a.tree ? tree_of<QMM_F16>(algo, head_dim, xtype, a, s) : attn_of<QMM_F16>(algo, head_dim, xtype, a, s);
+    case QMM_BF16: return a.tree ? tree_of<QMM_BF16>(algo, head_dim, xtype, a, s) : attn_of<QMM_BF16>(algo, head_dim, xtype, a, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -90,10 +90,6 @@ struct Staged {
     uint32_t vd[VT][Q8 ? 8 : 1];
 };
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
-}
 // What the lanes of block b (from lane 8 b on) hold.
 __device__ __forceinline__ float of_block(float x, int b) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 8 * b));
@@ -104,15 +100,22 @@ constexpr int group_of(int n, int most) { return n % most ? group_of(n, most - 1
 // Parts of Q and of P, and rows of a wave.
 constexpr int q_parts(int ct, bool xb) { return xb ? 1 : ct == QMM_BF16 ? 3 : 2; }
 constexpr int p_parts(int ct, bool xb) { return xb ? 2 : q_parts(ct, xb); }
-constexpr int wave_rows(int ct, int nb, bool xb) { return nb > 4 || q_parts(ct, xb) == 3 ? 16 : 32; }
+// With fewer rows than a tile of 128 has (trees of new tokens), two waves take the
+// same rows, and half of a tile's keys each; their sums are joined at the end.
+constexpr int wave_rows(int ct, int nb, bool xb, int rows = kTileRows) {
+    return nb > 4 || q_parts(ct, xb) == 3 || rows == 32 ? 16 : 32;
+}
+constexpr int halves_of(int rows) { return rows < kTileRows ? 2 : 1; }
+constexpr int waves_of(int ct, int nb, bool xb, int rows) { return rows / wave_rows(ct, nb, xb, rows) * halves_of(rows); }
 
-template <int CT, int NB, bool XB, bool TREE>
-__global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void attn_tile_kernel(AttnArgs a) {
+template <int CT, int NB, bool XB, bool TREE, int ROWS>
+__global__ __launch_bounds__(64 * waves_of(CT, NB, XB, ROWS), 2) void attn_tile_kernel(AttnArgs a) {
     constexpr int D = 32 * NB, RB = kv_row_bytes(CT, D);
     constexpr bool BF = CT == QMM_BF16, Q8 = CT == QMM_Q8_0;
     constexpr int AP = Q8 ? 2 : 1;                               // parts of K and V
     constexpr int QP = q_parts(CT, XB), PP = p_parts(CT, XB);    // of Q, of P
-    constexpr int R = wave_rows(CT, NB, XB), W = kTileRows / R;  // rows of a wave, waves
+    constexpr int R = wave_rows(CT, NB, XB, ROWS), W = waves_of(CT, NB, XB, ROWS);  // rows of a wave, waves
+    constexpr int HALVES = halves_of(ROWS), RG = W / HALVES;     // parts of a tile's keys, waves of each
     constexpr int GROUPS = 64 / R, KS = 8 * GROUPS;              // lanes of a row, values (or keys) of an MFMA's step
     constexpr int KPW = kKeys / W;                               // keys that a wave stages
     constexpr int VL = R * R / 64, NO = D / R;                   // values of an accumulator, accumulators
@@ -140,23 +143,24 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
     const TileAt at = w.at;
     const int lane = threadIdx.x & 63, r = lane % R, h = lane / R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = HALVES > 1 ? wave % RG : wave, half = HALVES > 1 ? wave / RG : 0;  // its rows, and its keys' half
     const int kvh = hb / a.chunks, G = a.n_q / a.c.n_kv;
     const int head0 = kvh * G + (hb % a.chunks) * a.chunk;
     const int heads = min(a.chunk, kvh * G + G - head0);
     const int rows = at.tokens * heads;
-    const int mr = min(R * wave + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
+    const int mr = min(R * rw + r, rows - 1), mt = mr / heads, head = head0 + mr % heads;
     TreeRow tree = {};
     if constexpr (TREE) tree = tree_row(a, at, mt);
     const int p_row = TREE ? tree.pos : at.pos + mt;
     // the positions of the wave's first and last row (in a tree, of any)
-    const int p_first = TREE ? at.base : at.pos + min(R * wave, rows - 1) / heads;
-    const int p_last = TREE ? at.kv - 1 : at.pos + min(R * wave + R - 1, rows - 1) / heads;
+    const int p_first = TREE ? at.base : at.pos + min(R * rw, rows - 1) / heads;
+    const int p_last = TREE ? at.kv - 1 : at.pos + min(R * rw + R - 1, rows - 1) / heads;
     const int all_see = TREE ? at.base : p_first + 1;  // every row of the wave sees the keys up to here
-    const bool idle = R * wave >= rows;
+    const bool idle = R * rw >= rows;
     // the key, in its tile, of value i of the lane's scores
     auto key_of = [&](int i) {
-        return R == 32 ? 32 * (i >> 4) + 8 * ((i & 15) >> 2) + 4 * h + (i & 3)
-                       : 32 * (i >> 3) + 8 * h + 4 * ((i >> 2) & 1) + (i & 3);
+        return (R == 32 ? 32 * (i >> 4) + 8 * ((i & 15) >> 2) + 4 * h + (i & 3)
+                        : 32 * (i >> 3) + 8 * h + 4 * ((i >> 2) & 1) + (i & 3)) + 32 * half;
     };
     // LDS offset of 16 bytes of K, columns col .. of 8 values.  (With 16 rows a wave the lanes of an operand
     // read the keys 0..3 of each 8: those of the upper half turn to other columns to miss the lower ones' banks,
@@ -239,7 +243,8 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 
     int64_t my_row = -1;  // lane i: where the wave's keys of tile i from here on begin in the cache, or -1
     St st;
-    // key j of the first of the wave's runs of 8 keys in the lanes' order (the second run begins 4 behind it)
+    // key j of the first of the wave's runs of 8 keys in the lanes' order (the second run begins RUN behind it)
+    constexpr int RUN = R == 32 ? 4 : 8;
     auto nth = [](int j) { return R == 32 ? (j & 3) + 2 * (j & 4) : j; };
     // Where the wave's keys of tile t begin in the cache, or -1.
     auto row_of = [&](int t) -> int64_t {
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         for (int i = 0; i < St::VT; ++i) {
             const uint32_t task = lane + 64 * i, oct = task / (8 * NB), c = task % (8 * NB);
             if (KPW * NB % 64 == 0 || task < KPW * NB) {
-                const uint32_t off = 4 * oct * RB + (Q8 ? (c >> 3) * kQ8_0Bytes : 8 * c);
+                const uint32_t off = RUN * oct * RB + (Q8 ? (c >> 3) * kQ8_0Bytes : 8 * c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const uint8_t* p = vbase + nth(j) * RB + off;
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
             for (int i = 0; i < St::VT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const bool ok = kept(row, key0 + 4 * ((lane + 64 * i) / (8 * NB)) + nth(j));
+                    const bool ok = kept(row, key0 + RUN * ((lane + 64 * i) / (8 * NB)) + nth(j));
                     if constexpr (Q8) {
                         st.vd[i][j] = ok ? st.vd[i][j] : 0;
                     } else {
@@ -441,19 +446,20 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
     };
 
-    constexpr int STEPS = D / KS, SUBS = kKeys / R;  // of an accumulator's products, accumulators of scores
-    constexpr int NK = SUBS * AP * STEPS, NV = kKeys / KS * NO * AP;  // A operands of a tile: of K and of V
+    constexpr int STEPS = D / KS, SUBS = kKeys / HALVES / R;  // of an accumulator's products, accumulators of scores
+    constexpr int NK = SUBS * AP * STEPS, VSTEPS = kKeys / HALVES / KS, NV = VSTEPS * NO * AP;  // A operands of a tile: of K and of V
+    constexpr int SC = R / HALVES;  // scores of a lane
     // operand i of K: (keys, part, values); of V: (step, values, part)
     auto k_operand = [&](int buf, int i) {
         const int u = i / (STEPS * AP), ap = AP - 1 - i / STEPS % AP, b = i % STEPS;
-        const int key = R == 32 ? 32 * u + r : 32 * (u >> 1) + 8 * (r >> 2) + 4 * (u & 1) + (r & 3);
+        const int key = (R == 32 ? 32 * u + r : 32 * (u >> 1) + 8 * (r >> 2) + 4 * (u & 1) + (r & 3)) + 32 * half;
         return *reinterpret_cast<const u4v*>(&s_k[AP * buf + ap][k_at(key, GROUPS * b + h)]);
     };
     auto v_operand = [&](int buf, int i) {
         const int kk = i / (NO * AP), c = i / AP % NO, ap = AP - 1 - i % AP, dim = R * c + r;
-        return *reinterpret_cast<const u4v*>(&s_v[AP * buf + ap][dim * (2 * kKeys) + 16 * v_slot(dim, GROUPS * kk + h)]);
+        return *reinterpret_cast<const u4v*>(&s_v[AP * buf + ap][dim * (2 * kKeys) + 16 * v_slot(dim, GROUPS * (kk + VSTEPS * half) + h)]);
     };
-    float s[R];
+    float s[SC];
     // From the products of tile t to scores (f s, times log2 e), masked; raises
     // the running maximum where they pass it by kSlack.
     auto soften = [&](int t, float& f) {
@@ -461,6 +467,10 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         bool page[4];  // of each 16 keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) page[i] = s_page[t & 1][W / 4 * i] != 0;
+        if constexpr (HALVES > 1) {  // of its keys
+            page[0] = half ? page[2] : page[0], page[1] = half ? page[3] : page[1];
+            page[2] = page[0], page[3] = page[1];
+        }
         if (capped) {
             cap_scores(s, f, a.softcap);
             f = 1.0f;
@@ -470,16 +480,16 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         auto place = [&](int key) { return TREE && kb + kKeys > at.base ? tree_place(at, tree, key) : key; };
         if (a.slopes) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) s[i] = s[i] * f - slope * fabsf((float)(p_row - place(kb + key_of(i))));
+            for (int i = 0; i < SC; ++i) s[i] = s[i] * f - slope * fabsf((float)(p_row - place(kb + key_of(i))));
             f = 1.0f;
         }
         if (!whole) {
-            const uint64_t bits = TREE ? tree_bits(a, at, tree, kb) >> (R == 32 ? 4 * h : 8 * h) : 0;
+            const uint64_t bits = TREE ? tree_bits(a, at, tree, kb) >> ((R == 32 ? 4 * h : 8 * h) + 32 * half) : 0;
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
+            for (int i = 0; i < SC; ++i) {
                 const int key = kb + key_of(i);
                 const bool paged = R == 32 ? page[i >> 3] : (h >> 1 ? page[2 * (i >> 3) + 1] : page[2 * (i >> 3)]);
-                const bool near = TREE ? (bits >> (key_of(i) - (R == 32 ? 4 * h : 8 * h)) & 1) &
+                const bool near = TREE ? (bits >> (key_of(i) - (R == 32 ? 4 * h : 8 * h) - 32 * half) & 1) &
                                              (a.window <= 0 || p_row - place(key) < reach)
                                        : (key <= p_row) & (p_row - key < reach);
                 const bool seen = paged & (key < at.len) & (near | (key < at.pre));
@@ -488,7 +498,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
         float big = s[0];
 #pragma unroll
-        for (int i = 1; i < R; ++i) big = fmaxf(big, s[i]);
+        for (int i = 1; i < SC; ++i) big = fmaxf(big, s[i]);
         if (__any(big * f > mx + kSlack)) {
             if constexpr (R == 16) big = fmaxf(big, __shfl_xor(big, 16));
             big = fmaxf(big, __shfl_xor(big, 32)) * f;
@@ -552,7 +562,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int i = 0; i < R; ++i) s[i] = acc[i / VL][i % VL];
+            for (int i = 0; i < SC; ++i) s[i] = acc[i / VL][i % VL];
         }
         u4v vf[2][GV];
 #pragma unroll
@@ -560,7 +570,7 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         __builtin_amdgcn_sched_barrier(0);
         soften(t, f);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / KS; ++kk) {
+        for (int kk = 0; kk < VSTEPS; ++kk) {
             u4v pf[PP];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -591,17 +601,46 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
         }
     }
 
+    if constexpr (HALVES > 1) {
+        // the second half's sums go to the first's waves, through what held K
+        static_assert(sizeof(s_k) >= ROWS * D * 4, "a half's sums");
+        __shared__ float s_ml[2][RG][64];
+        f4v(*s_o)[NO * VL / 4][64] = reinterpret_cast<f4v(*)[NO * VL / 4][64]>(&s_k[0][0]);
+        __syncthreads();
+        if (half) {
+            s_ml[0][rw][lane] = mx, s_ml[1][rw][lane] = l;
+#pragma unroll
+            for (int c = 0; c < NO; ++c)
+#pragma unroll
+                for (int i = 0; i < VL; i += 4)
+                    s_o[rw][(c * VL + i) / 4][lane] = f4v{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]};
+        }
+        __syncthreads();
+        if (half) return;
+        const float other = s_ml[0][rw][lane], top = fmaxf(mx, other), ref = top == -INFINITY ? 0.f : top;
+        const float f0 = __builtin_amdgcn_exp2f(mx - ref), f1 = __builtin_amdgcn_exp2f(other - ref);
+        mx = top;
+        l = f0 * l + f1 * s_ml[1][rw][lane];
+#pragma unroll
+        for (int c = 0; c < NO; ++c)
+#pragma unroll
+            for (int i = 0; i < VL; i += 4) {
+                const f4v x = s_o[rw][(c * VL + i) / 4][lane];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[c][i + j] = f0 * o[c][i + j] + f1 * x[j];
+            }
+    }
     if constexpr (R == 16) l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (R * wave + r >= rows) return;
+    if (R * rw + r >= rows) return;
     const int64_t row = (int64_t)(at.row + mt) * a.n_q + head;
     const float lane_unit = Q8 ? ldexpf(1.0f, vex - 8) : 1.0f;
     auto unit = [&](int c) { return Q8 ? of_block(lane_unit, R * c / 32) : 1.0f; };
     if (a.splits && h == 0 && w.split == 0)
-        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * a.slots + R * wave + r};
+        join_of(a)[row] = JoinOf{w.first, w.splits > 1 ? w.splits : 0, w.step, hb * a.slots + R * rw + r};
     // accumulator c, value i: value R c + 8 (i / 4) + 4 h + i % 4 of the row
     if (w.splits > 1) {
-        const int64_t part = ((int64_t)item * groups + hb) * a.slots + R * wave + r;
+        const int64_t part = ((int64_t)item * groups + hb) * a.slots + R * rw + r;
         float* ml = a.work + a.parts * D;
         if (h == 0) ml[2 * part] = mx, ml[2 * part + 1] = l;
 #pragma unroll
@@ -636,8 +675,17 @@ __global__ __launch_bounds__(64 * kTileRows / wave_rows(CT, NB, XB), 2) void att
 template <int CT, int NB, bool XB, bool TREE>
 hipError_t tile_typed(const AttnArgs& a, hipStream_t s) {
     const int64_t grid = a.items * a.c.n_kv * a.chunks;  // below 2^32 work-items
-    hipError_t e = launch(attn_tile_kernel<CT, NB, XB, TREE>, dim3((unsigned)grid), dim3(64 * kTileRows / wave_rows(CT, NB, XB)), 0,
-                          s, a);
+    hipError_t e;
+    if constexpr (TREE) {
+        if (NB <= 4 && a.tile_rows == 32)
+            e = launch(attn_tile_kernel<CT, NB, XB, TREE, NB <= 4 ? 32 : 64>, dim3((unsigned)grid),
+                       dim3(64 * waves_of(CT, NB, XB, 32)), 0, s, a);
+        else
+            e = launch(attn_tile_kernel<CT, NB, XB, TREE, 64>, dim3((unsigned)grid), dim3(64 * waves_of(CT, NB, XB, 64)), 0, s, a);
+    } else {
+        e = launch(attn_tile_kernel<CT, NB, XB, TREE, kTileRows>, dim3((unsigned)grid),
+                   dim3(64 * waves_of(CT, NB, XB, kTileRows)), 0, s, a);
+    }
     return e != hipSuccess || !a.splits ? e : launch_attn_join(32 * NB, XB ? QMM_BF16 : QMM_F32, a, s);
 }
 

@@ -14,7 +14,7 @@ namespace {
 
 // How qmm_attn divides its work.
 struct Plan {
-    int algo, chunk, chunks, shift, splits, least, slots;
+    int algo, chunk, chunks, shift, splits, least, slots, rows;
     int64_t items, parts;
 };
 
@@ -65,11 +65,81 @@ int choose(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o,
     return tile < split ? 2 : 1;
 }
 
-Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int xtype, int n_q) {
+// Parts that the split kernels divide the keys of a head's row tiles in.
+int64_t split_parts(const qmm_kv_cache* c, int64_t tiles, int64_t heads, int64_t keys) {
+    const int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
+    const int64_t slots = c->head_dim > 128 ? 512 : 768, rest = slots - tiles * heads;
+    const int64_t low = rest < 256 || rest > 512 ? 512 : rest;
+    return up_div(s < low ? low : s > 2048 ? 2048 : s, heads);
+}
+
+// Row tiles of `rows` rows, over all heads, as far as the host knows.
+int64_t row_tiles(const qmm_kv_batch* b, int n_kv, int G, int rows) {
+    const int chunk = G < rows ? G : rows;
+    const int64_t each = up_div(b->n_tokens, b->n_seqs);
+    return up_div(each, int64_t(1) << tile_tokens(rows, chunk, each)) * b->n_seqs * n_kv * up_div(G, chunk);
+}
+
+// Trees of new tokens have some rows a sequence, over long caches: 2 to 100
+// tokens of 1 to 32 heads a key-value head.  Split kernels take 16 of them, the
+// kernels of Q8_0 rows 32, the tile kernels 32 or 64 (heads above 128, which stage
+// 8 keys a wave: 64).  In units of 1000 products of a row tile with 32 keys of 64
+// values, their times over 180 drawn sizes are some 12 us (17 for wide heads) and 0.9
+// us a unit, 3 us more and 0.9 a unit (of half as many), 1 us more and 1.7 a unit.
+// The choice by these costs 4 to 7% (geometric mean) against the better one of
+// each size.  us, split against the others: 8 drafts over 8000 keys, 32 sequences, 32
+// heads on 8 of 128, Q8_0 180, 155; the same bf16 over bf16 221, 160; 13 drafts over 130911
+// keys in fp16 193, 113; 26 over 3100, 12 sequences, 16 heads on 8 of 256, bf16 164, 59;
+// 12 over 2000 of 14 heads on 2 of 64, Q8_0 16.1, 17.5; 62 over 61, fp32 over fp16, 10.6, 15.4.
+// Heads of 96, 192 and 256 over Q8_0 stay with the split kernels (256, above 4000 keys:
+// half of the tile kernels' time), which is why those have no form for Q8_0 here.
+Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int xtype, int n_q) {
+    Plan p = {};
+    const int G = n_q / c->n_kv;
+    const bool q8 = c->type == QMM_Q8_0, only_split = q8 && c->head_dim != 64 && c->head_dim != 128;
+    const int64_t each = up_div(b->n_tokens, b->n_seqs);
+    const int rows = q8 || (c->head_dim <= 128 && each * G <= 32) ? 32 : 64;
+    int64_t keys = key_bound(c, b);
+    if (o->window > 0 && !o->prefix && o->window + each < keys) keys = o->window + each;
+    const double unit = 1e-3 * (double)keys / 32 * (c->head_dim / 64.0);
+    const double split = 0.9 * unit * (double)row_tiles(b, c->n_kv, G, kSplitRows);
+    const double other = (q8 ? 3.0 : 1.0) + (q8 ? 0.9 : 1.7) * unit * (double)row_tiles(b, c->n_kv, G, rows);
+    p.algo = only_split ? 1 : o->algo ? o->algo : other < split ? 2 : 1;
+    p.rows = p.algo == 1 ? kSplitRows : rows;
+    p.chunk = G < p.rows ? G : p.rows;
+    p.chunks = (int)up_div(G, p.chunk);
+    p.shift = tile_tokens(p.rows, p.chunk, each);
+    int64_t tiles = (b->n_tokens >> p.shift) + b->n_seqs;  // row tiles of a head at most
+    if (tiles > b->n_tokens) tiles = b->n_tokens;
+    const int64_t heads = (int64_t)c->n_kv * p.chunks;
+    p.least = 4;
+    const int64_t most = tiles * up_div(keys, 32 * p.least);
+    int64_t s;
+    if (p.algo == 1) {
+        s = split_parts(c, tiles, heads, keys);
+    } else {
+        // As many workgroups as run at once (two a CU, one of eight waves), a row tile's parts being some half more
+        // than the whole ones; twice as many where sequences are long and uneven (Q8_0, 128 values, above 4000 keys: 10%
+        // faster; one sequence of 7930: 50 us against 62).  Up to 512 keys the join would cost more than it saves.
+        const bool eight = p.rows == 64 && (c->head_dim > 128 || (c->type == QMM_BF16 && xtype == QMM_F32));
+        const int64_t run = eight ? 256 : q8 && c->head_dim == 128 && keys > 4000 && b->n_seqs > 1 ? 1024 : 512;
+        s = up_div(run, heads) - tiles / 2;
+        if (keys <= 512 || s <= tiles / 2) s = 0;
+    }
+    if (s > most) s = most;
+    p.splits = keys > 32 * p.least ? (int)s : 0;
+    p.items = tiles + p.splits;
+    p.slots = p.chunk << p.shift;
+    p.parts = p.splits ? p.items * heads * p.slots : 0;
+    return p;
+}
+
+Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int xtype, int n_q, bool tree) {
+    if (tree) return plan_tree(c, b, o, xtype, n_q);
     Plan p = {};
     const int G = n_q / c->n_kv;
     p.algo = o->algo ? o->algo : choose(c, b, o, n_q);
-    const int rows = p.algo == 2 ? kTileRows : kSplitRows;
+    const int rows = p.rows = p.algo == 2 ? kTileRows : kSplitRows;
     p.chunk = G < rows ? G : rows;
     p.chunks = (int)up_div(G, p.chunk);
     p.shift = tile_tokens(rows, p.chunk, up_div(b->n_tokens, b->n_seqs));
@@ -99,10 +169,7 @@ Plan plan(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, 
     p.least = 4;
     const bool heavy = c->head_dim > 128 && (c->type == QMM_Q8_0 || (c->type == QMM_BF16 && xtype == QMM_F32));
     const int64_t heads = (int64_t)c->n_kv * p.chunks, most = tiles * up_div(keys, 32 * p.least);
-    int64_t s = tiles * heads * up_div(keys, 64) / 32;  // (below 2^60)
-    const int64_t slots = c->head_dim > 128 ? 512 : 768, rest = slots - tiles * heads;
-    const int64_t low = p.algo == 2 || rest < 256 || rest > 512 ? 512 : rest;
-    s = up_div(s < low || p.algo == 2 ? low : s > 2048 ? 2048 : s, heads);
+    int64_t s = p.algo == 2 ? up_div(512, heads) : split_parts(c, tiles, heads, keys);
     if (s > most) s = most;
     p.splits = keys > 32 * p.least && (p.algo == 1 || s >= 4 * tiles || (heavy && s > tiles)) ? (int)s : 0;
     p.items = tiles + p.splits;
@@ -146,7 +213,7 @@ int attend(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_kv_tr
     if ((rc = check_xtype(xtype)) || (rc = check_cache(cache)) || (rc = check_batch(cache, batch))) return rc;
     if ((rc = check_attn_sizes(cache, batch, xtype, n_q)) || (rc = check_opts(opts))) return rc;
     if ((rc = check_rows(q, ldq, batch->n_tokens, n_q, cache->head_dim)) || (rc = check_ptr(out))) return rc;
-    const Plan p = plan(cache, batch, opts, xtype, n_q);
+    const Plan p = plan(cache, batch, opts, xtype, n_q, tree != nullptr);
     if (!fits(cache, batch, n_q, p)) return QMM_ERR_SHAPE;
     const size_t need = work_bytes_of(cache, batch, n_q, p);
     if (need) {
@@ -178,6 +245,7 @@ int attend(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_kv_tr
         a.tree = tree->seen;
         a.depth = tree->depth;
         a.words = tree->words;
+        a.tile_rows = p.rows;
     }
     return hip_status(launch_attn(p.algo, cache->type, cache->head_dim, xtype, a, static_cast<hipStream_t>(stream)));
 }
@@ -252,20 +320,22 @@ int qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qm
 int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xtype, int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q)) return 0;
     const qmm_attn_opts none = {};
-    const Plan p = plan(cache, batch, &none, xtype, n_q);
+    const Plan p = plan(cache, batch, &none, xtype, n_q, false);
     return fits(cache, batch, n_q, p) ? p.algo : 0;
 }
 
 size_t qmm_attn_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
                      int n_q) {
     if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
-    const Plan p = plan(cache, batch, opts, xtype, n_q);
+    const Plan p = plan(cache, batch, opts, xtype, n_q, false);
     return fits(cache, batch, n_q, p) ? work_bytes_of(cache, batch, n_q, p) : 0;
 }
 
 size_t qmm_attn_tree_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype,
                           int n_q) {
-    return qmm_attn_work(cache, batch, opts, xtype, n_q);
+    if (check_attn_sizes(cache, batch, xtype, n_q) || check_opts(opts)) return 0;
+    const Plan p = plan(cache, batch, opts, xtype, n_q, true);
+    return fits(cache, batch, n_q, p) ? work_bytes_of(cache, batch, n_q, p) : 0;
 }
 
 int qmm_attn(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_attn_opts* opts, int xtype, const void* q,

@@ -57,6 +57,7 @@ struct AttnArgs {
     const uint64_t* tree;
     const int32_t* depth;
     int32_t words;
+    int32_t tile_rows;  // of the tile kernels: 32, 64 or 128
 };
 
 // What builds a tree from its tokens' parents.
@@ -129,6 +130,7 @@ template <int CT, bool TREE>
 hipError_t launch_attn_tile_narrow(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 template <int CT, bool TREE>
 hipError_t launch_attn_tile_wide(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_tree_q8_0(int head_dim, int xtype, const AttnArgs& a, hipStream_t s);
 hipError_t launch_kv_tree(const TreeArgs& a, hipStream_t s);
 hipError_t launch_kv_copy(int layers, const LayerArgs& l, const CopyArgs& a, hipStream_t s);
 hipError_t launch_kv_compact(int type, int head_dim, int layers, const LayerArgs& l, const CompactArgs& a, hipStream_t s);
