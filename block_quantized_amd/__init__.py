@@ -761,13 +761,14 @@ def logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, softcap: flo
 
 
 def _logprobs(logits, xtype, ld, rows, vocab, tokens, top, scale, softcap, handle):
-    L, given = lib(), 0 if tokens is None else tokens.shape[1]
-    new = logits.new_empty
+    L, given, dev = lib(), 0 if tokens is None else tokens.shape[1], logits.device
     need = L.qmm_logprobs_work(xtype, rows, vocab, top)
-    logp = new((rows, given), dtype=_torch.float32) if tokens is not None else None
-    entropy = new(rows, dtype=_torch.float32)
-    ids, best = (new((rows, top), dtype=_torch.int32), new((rows, top), dtype=_torch.float32)) if top else (None, None)
-    work = new(need, dtype=_torch.uint8) if need else None
+    new, f32 = _torch.empty_strided, _torch.float32  # (0.3 us less each than empty)
+    logp = new((rows, given), (given, 1), dtype=f32, device=dev) if tokens is not None else None
+    entropy = new((rows,), (1,), dtype=f32, device=dev)
+    ids = new((rows, top), (top, 1), dtype=_torch.int32, device=dev) if top else None
+    best = new((rows, top), (top, 1), dtype=f32, device=dev) if top else None
+    work = new((need,), (1,), dtype=_torch.uint8, device=dev) if need else None
     rc = L.qmm_logprobs(xtype, logits.data_ptr(), ld, rows, vocab, scale, softcap, _ptr(tokens), given, _ptr(logp),
                         entropy.data_ptr(), top, _ptr(ids), _ptr(best), _ptr(work), need, handle)
     if rc != QMM_OK:

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(LayerArgs l, CompactArg
     using U = Unit<RB>;
     constexpr int UNITS = RB / (int)sizeof(U), PER = 4;  // units of a row, and of a lane in a chunk
     constexpr int ROWS = 256 * PER / UNITS;              // rows of a chunk
-    __shared__ int64_t s_from[ROWS], s_to[ROWS];
+    __shared__ int64_t s_from[2][ROWS], s_to[2][ROWS];
     const int s = blockIdx.x / a.n_kv, head = blockIdx.x % a.n_kv;
     const int64_t first = a.first[s];
     const int n = min(max(a.n_keep[s], 0), a.width);
@@ -78,30 +78,37 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(LayerArgs l, CompactArg
         if (pg < 0 || pg >= a.n_pages) return -1;
         return (((int64_t)pg * a.n_kv + head) * a.page_size + ((int)j - nth * a.page_size)) * RB;
     };
-    for (int c = 0; c < n; c += ROWS) {
-        const int rows = min(ROWS, n - c);
-        __syncthreads();  // the places of the chunk before are read
-        for (int i = threadIdx.x; i < rows; i += 256) {
-            const int64_t j = a.keep[(int64_t)s * a.width + c + i];
+    // the places of chunk c's rows, which the workgroup reads after the next barrier
+    auto look_up = [&](int c) {
+        for (int i = threadIdx.x; i < ROWS; i += 256) {
             int64_t from = -1, to = -1;
-            if (j != first + c + i) from = row_of(j), to = row_of(first + c + i);
-            s_from[i] = to < 0 ? -1 : from;
-            s_to[i] = to;
+            if (c + i < n) {
+                const int64_t j = a.keep[(int64_t)s * a.width + c + i];
+                if (j != first + c + i) from = row_of(j), to = row_of(first + c + i);
+            }
+            s_from[c / ROWS & 1][i] = to < 0 ? -1 : from;
+            s_to[c / ROWS & 1][i] = to;
         }
-        __syncthreads();
+    };
+    if (n > 0) look_up(0);
+    __syncthreads();
+    for (int c = 0; c < n; c += ROWS) {
+        const int b = c / ROWS & 1;
         U x[PER];
+        int64_t to[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int u = 256 * k + threadIdx.x, i = u / UNITS;
-            if (i < rows && s_from[i] >= 0) x[k] = reinterpret_cast<const U*>(pool + s_from[i])[u % UNITS];
+            const int64_t from = i < ROWS ? s_from[b][i] : -1;
+            to[k] = from < 0 ? -1 : s_to[b][i] + u % UNITS * (int)sizeof(U);
+            if (from >= 0) x[k] = reinterpret_cast<const U*>(pool + from)[u % UNITS];
         }
+        if (c + ROWS < n) look_up(c + ROWS);  // while the rows are on their way
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // every wave's rows have come before one is overwritten
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int u = 256 * k + threadIdx.x, i = u / UNITS;
-            if (i < rows && s_from[i] >= 0) reinterpret_cast<U*>(pool + s_to[i])[u % UNITS] = x[k];
-        }
+        for (int k = 0; k < PER; ++k)
+            if (to[k] >= 0) *reinterpret_cast<U*>(pool + to[k]) = x[k];
     }
 }
 

@@ -30,8 +30,35 @@ typedef unsigned long long rank_t;
 
 constexpr float kLog2 = 0.69314718055994530942f, kInvLog2 = 1.44269504088896340736f;
 
-// Sums of some of a row's values: m is a logit (capped, not scaled), E is in
-// units of log 2.  unit: the scale, in these.
+// What lane ^ M holds.
+template <int CTRL, int BANKS = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, 0xF, BANKS, false);
+}
+template <int M>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+    if constexpr (M == 1) return dpp<0xB1>(x, x);
+    if constexpr (M == 2) return dpp<0x4E>(x, x);
+    if constexpr (M == 4) return dpp<0x114, 0xA>(dpp<0x104, 0x5>(x, x), x);  // 4 lanes up, and 4 down
+    if constexpr (M == 8) return dpp<0x128>(x, x);                           // a turn by 8 of each 16
+    if constexpr (M >= 16) {
+        // the halves of two copies change places: one then holds the even rows (or lower half) twice, one the odd ones
+        const auto r = M == 16 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
+                               : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return (threadIdx.x & M) ? r[0] : r[1];
+    }
+}
+template <int M>
+__device__ __forceinline__ float lane_xor(float x) {
+    return __builtin_bit_cast(float, lane_xor<M>(__builtin_bit_cast(uint32_t, x)));
+}
+template <int M>
+__device__ __forceinline__ rank_t lane_xor(rank_t k) {
+    return (rank_t)lane_xor<M>((uint32_t)(k >> 32)) << 32 | lane_xor<M>((uint32_t)k);
+}
+
+// Sums of some of a row's values: m is the largest of them, E is in units of
+// log 2.  unit: what a difference of values is in these.
 struct Sums {
     float m, rest, ent;
 };
@@ -43,8 +70,10 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b, float unit) {
     const float f = __builtin_amdgcn_exp2f(gap), one = 1.0f + lo.rest;
     return Sums{hi.m, hi.rest + f * one, hi.ent + f * (lo.ent - fmaxf(gap, -16384.0f) * one)};
 }
-__device__ __forceinline__ Sums shuffled(Sums s, int k) {
-    return Sums{__shfl_xor(s.m, k), __shfl_xor(s.rest, k), __shfl_xor(s.ent, k)};
+template <int M>
+__device__ __forceinline__ Sums merged_lanes(Sums s, float unit) {
+    if constexpr (M < 32) s = merged_lanes<M * 2>(s, unit);
+    return merge(s, Sums{lane_xor<M>(s.m), lane_xor<M>(s.rest), lane_xor<M>(s.ent)}, unit);
 }
 
 // A logit as a whole number of the same order; a NaN counts as -inf.
@@ -53,51 +82,53 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float unordered(uint32_t u) {  // (no NaN's)
+    return __builtin_bit_cast(float, u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+}
 __device__ __forceinline__ rank_t key_of(float x, uint32_t id) { return (rank_t)ordered(x) << 32 | (uint32_t)~id; }
 __device__ __forceinline__ rank_t lane_key(rank_t k, int lane) {  // lane: the same in all lanes
     return (rank_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32 |
            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, lane);
 }
-__device__ __forceinline__ rank_t xor_key(rank_t k, int mask) {
-    return (rank_t)(uint32_t)__shfl_xor((int)(k >> 32), mask) << 32 | (uint32_t)__shfl_xor((int)(uint32_t)k, mask);
-}
 // One step of a bitonic sort: the larger of two lanes' keys to the lower lane, or to the upper one.
-__device__ __forceinline__ rank_t exchange(rank_t k, int mask, bool larger) {
-    const rank_t o = xor_key(k, mask);
+template <int M, typename T>
+__device__ __forceinline__ T exchange(T k, bool larger) {
+    const T o = lane_xor<M>(k);
     return (k > o) == larger ? k : o;
 }
-__device__ __forceinline__ rank_t sorted(rank_t k, int lane) {  // descending from lane 0 on
-#pragma unroll
-    for (int n = 2; n <= 64; n <<= 1)
-#pragma unroll
-        for (int m = n / 2; m >= 1; m >>= 1) k = exchange(k, m, ((lane & m) == 0) == ((lane & n) == 0 || n == 64));
+template <int N, int M, typename T>
+__device__ __forceinline__ T sort_steps(T k, int lane) {
+    k = exchange<M>(k, ((lane & M) == 0) == ((lane & N) == 0 || N == 64));
+    if constexpr (M > 1) k = sort_steps<N, M / 2>(k, lane);
     return k;
 }
-// The 64 largest of two sorted lists, sorted.
-__device__ __forceinline__ rank_t joined(rank_t a, rank_t b, int lane) {
-    const rank_t o = xor_key(b, 63);  // b's from its last one on
-    rank_t k = a > o ? a : o;
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) k = exchange(k, m, (lane & m) == 0);
-    return k;
+template <int N, typename T>
+__device__ __forceinline__ T sorted(T k, int lane) {  // descending from lane 0 on, of each N lanes
+    if constexpr (N > 2) k = sorted<N / 2>(k, lane);
+    return sort_steps<N, N / 2>(k, lane);
 }
+// The 64 largest of two sorted lists, sorted; `b` from its last one on.
+__device__ __forceinline__ rank_t joined(rank_t a, rank_t b, int lane) { return sort_steps<64, 32>(a > b ? a : b, lane); }
 // A sorted list with one key more.
 __device__ __forceinline__ rank_t inserted(rank_t list, rank_t k, int lane) {
     const int at = __popcll(__ballot(list > k));
-    const rank_t up = (rank_t)(uint32_t)__shfl_up((int)(list >> 32), 1) << 32 | (uint32_t)__shfl_up((int)(uint32_t)list, 1);
+    const rank_t up = (rank_t)dpp<0x138>(0, (uint32_t)(list >> 32)) << 32 | dpp<0x138>(0, (uint32_t)list);  // of lane - 1
     return lane < at ? list : lane == at ? k : up;
 }
 
-// x = cap tanh(x / cap), 2^-22 off relative to the larger of itself and 0.35 cap; -inf stays.
-__device__ __forceinline__ float capped(float x, float cap, float inv) {
-    const float y = x * inv, a = fabsf(y), y2 = y * y;
+// tanh y, 2^-22 off relative to the larger of itself and 0.35; -inf stays.  SMALL:
+// below 0.35, where the polynomial in y^2 that is closest to tanh(y) / y does.
+template <bool SMALL>
+__device__ __forceinline__ float tanh_of(float y) {
+    const float y2 = y * y;
     float p = fmaf(0.0193613345f, y2, -0.0537063462f);
     p = fmaf(p, y2, 0.133322014f);
     p = fmaf(p, y2, -0.333333161f);
     const float small = fmaf(p * y2, y, y);
-    const float e = __builtin_amdgcn_exp2f(2.0f * kInvLog2 * a);
+    if constexpr (SMALL) return small;
+    const float a = fabsf(y), e = __builtin_amdgcn_exp2f(2.0f * kInvLog2 * a);
     const float large = copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), y);
-    return x == -INFINITY ? x : cap * (a < 0.35f ? small : large);
+    return y == -INFINITY ? y : a < 0.35f ? small : large;
 }
 
 __device__ __forceinline__ float bf16_f32(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
@@ -113,13 +144,12 @@ __device__ __forceinline__ float logit(const LogprobArgs& a, int64_t row, int v)
 template <bool BF>
 __device__ void finish(const LogprobArgs& a, int64_t row, Sums s, rank_t list) {
     const int lane = threadIdx.x & 63;
-    const float inv = a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
+    const bool cap = a.softcap > 0.f;
+    const float inv = cap ? 1.0f / a.softcap : 0.f, unit = cap ? a.scale * a.softcap : a.scale;
     const float lse = log1pf(s.rest);
     auto logp = [&](float x) {
-        if (a.softcap > 0.f) x = capped(x, a.softcap, inv);
-        // the same product as the sums': the largest one's is exactly m
-        const float gap = s.m == -INFINITY ? -INFINITY : (x - s.m) * a.scale;
-        return gap - lse;
+        if (cap) x = tanh_of<false>(x * inv);
+        return (s.m == -INFINITY ? -INFINITY : (x - s.m) * unit) - lse;
     };
     for (int i = threadIdx.x; i < a.given; i += blockDim.x) {
         const int t = a.tokens[row * a.given + i];
@@ -131,6 +161,27 @@ __device__ void finish(const LogprobArgs& a, int64_t row, Sums s, rank_t list) {
         a.top_ids[row * a.top + lane] = (int32_t)id;
         a.top_logp[row * a.top + lane] = logp(logit<BF>(a, row, (int)id));
     }
+}
+
+// The wavefronts' sums and lists, joined: the sums in every lane, the list in
+// the first wavefront.
+__device__ __forceinline__ void join_waves(const LogprobArgs& a, float unit, int wave, int lane, Sums& sums, rank_t& list) {
+    __shared__ Sums s_sums[kLogitWaves];
+    __shared__ rank_t s_list[kLogitWaves][64];
+    static_assert(kLogitWaves == 4, "two rounds");
+    sums = merged_lanes<1>(sums, unit);
+    if (lane == 0) s_sums[wave] = sums;
+    if (a.top && wave >= 2) s_list[wave][lane] = list;
+    __syncthreads();
+    if (a.top && wave < 2) {
+        list = joined(list, s_list[wave + 2][63 - lane], lane);
+        if (wave == 1) s_list[1][lane] = list;
+    }
+    __syncthreads();
+    if (a.top && wave == 0) list = joined(list, s_list[1][63 - lane], lane);
+    sums = s_sums[0];
+#pragma unroll
+    for (int w = 1; w < kLogitWaves; ++w) sums = merge(sums, s_sums[w], unit);
 }
 
 template <bool BF, bool CAP>
@@ -147,15 +198,13 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a) {
     base -= skew * (BF ? 2 : 4);
     const int q0 = skew ? 1 : 0, q1 = max((a.vocab + skew) / N, q0);
     const int from = part ? part * (a.part / N) : q0, upto = min((part + 1) * (a.part / N), q1);
-    const float inv = CAP ? 1.0f / a.softcap : 0.f, unit = a.scale * kInvLog2;
+    const float inv = CAP ? 1.0f / a.softcap : 0.f, unit = a.scale * kInvLog2 * (CAP ? a.softcap : 1.0f);
 
     Sums sums = {-INFINITY, 0.f, 0.f};
     rank_t list = 0, least = 0;  // the largest keys, and the last wanted one of them (0: there are fewer)
     auto add = [&](rank_t k) {   // a key each
-        for (uint64_t todo = __ballot(k > least); todo; todo &= todo - 1) {
-            const rank_t one = lane_key(k, __ffsll((unsigned long long)todo) - 1);
-            if (one <= least) continue;
-            list = inserted(list, one, lane);
+        for (uint64_t todo = __ballot(k > least); todo; todo = __ballot(k > least) & todo & (todo - 1)) {
+            list = inserted(list, lane_key(k, __ffsll((unsigned long long)todo) - 1), lane);
             const rank_t last = lane_key(list, a.top - 1);
             least = last > least ? last : least;
         }
@@ -164,37 +213,46 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a) {
         const bool on = v0 + lane < v1;
         const float x = on ? logit<BF>(a, row, v0 + lane) : -INFINITY;
         if (a.top) add(on ? key_of(x, v0 + lane) : 0);
-        const float y = CAP ? capped(x, a.softcap, inv) : x;
+        const float y = CAP ? tanh_of<false>(x * inv) : x;
         // (a NaN or +inf: the row's sums are NaN)
         sums = merge(sums, Sums{y, y < INFINITY ? 0.f : NAN, 0.f}, unit);
     };
     const int head = min(q0 * N - skew, a.vocab), tail = max(q1 * N - skew, head);
     if (part == 0 && wave == 0) few(0, head);
-    for (int at = from + wave * (kSegment / N); at < upto; at += kLogitWaves * (kSegment / N)) {
+    // (bf16: the next segment's loads go ahead of this one's arithmetic, 298 -> 281 us for 2048 rows of 151936 with a cap;
+    // fp32 values stay in the registers they were loaded to, and the waves' number hides the loads: 36 us for 257 rows of
+    // 128256, 39 with loads ahead)
+    u4v w[LOADS];
+    auto load = [&](int at) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+            w[j] = *reinterpret_cast<const u4v*>(base + 16 * (int64_t)min(at + 64 * j + lane, upto - 1));
+    };
+    int at = from + wave * (kSegment / N);
+    if (BF && at < upto) load(at);
+    for (; at < upto; at += kLogitWaves * (kSegment / N)) {
+        if (!BF) load(at);
         float x[kLaneValues];
-        {
-            u4v w[LOADS];
-            bool on[LOADS];
+        auto unpack = [&](int j, bool on) {
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) {
-                const int q = at + 64 * j + lane;
-                on[j] = q < upto;
-                w[j] = *reinterpret_cast<const u4v*>(base + 16 * (int64_t)(on[j] ? q : upto - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (BF) {
-                        x[N * j + 2 * i] = on[j] ? bf16_f32(w[j][i] & 0xFFFF) : -INFINITY;
-                        x[N * j + 2 * i + 1] = on[j] ? bf16_f32(w[j][i] >> 16) : -INFINITY;
-                    } else {
-                        // (a bit_cast of the element itself takes the vector's first one: ROCm 7.2's compiler)
-                        const uint32_t u = w[j][i];
-                        x[N * j + i] = on[j] ? __builtin_bit_cast(float, u) : -INFINITY;
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t u = w[j][i];  // (a bit_cast of the element itself takes the vector's first one: ROCm 7.2's compiler)
+                if constexpr (BF) {
+                    x[N * j + 2 * i] = on ? bf16_f32(u & 0xFFFF) : -INFINITY;
+                    x[N * j + 2 * i + 1] = on ? __builtin_bit_cast(float, u & 0xFFFF0000u) : -INFINITY;
+                } else {
+                    x[N * j + i] = on ? __builtin_bit_cast(float, u) : -INFINITY;
                 }
+            }
+        };
+        if (at + 64 * LOADS <= upto) {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) unpack(j, true);
+        } else {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) unpack(j, at + 64 * j + lane < upto);
         }
+        if (BF && at + kLogitWaves * (kSegment / N) < upto) load(at + kLogitWaves * (kSegment / N));
         float big = x[0];
 #pragma unroll
         for (int i = 1; i < kLaneValues; ++i) big = fmaxf(big, x[i]);
@@ -208,60 +266,54 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a) {
                     return q < upto ? key_of(x[i], (uint32_t)(q * N + i % N - skew)) : 0;
                 };
                 if (!least || __popcll(pass) > 12) {
-                    rank_t k = 0;
-#pragma unroll
-                    for (int i = 0; i < kLaneValues; ++i) {
-                        const rank_t o = key(i);
-                        k = o > k ? o : k;
-                    }
-                    k = lane_key(sorted(k, lane), a.top - 1);
-                    least = k > least ? k - 1 : least;  // (that key itself is wanted)
+                    // as many lanes hold a value of at least the last wanted one of the lanes' largest
+                    const uint32_t mine = at + lane < upto ? ordered(big) : 0;
+                    const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)sorted<64>(mine, lane), a.top - 1);
+                    const rank_t below = last ? ((rank_t)last << 32) - 1 : 0;
+                    least = below > least ? below : least;
                 }
+                const float bar = least >> 32 ? unordered((uint32_t)(least >> 32)) : -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kLaneValues; ++i) add(key(i));
+                for (int i = 0; i < kLaneValues; ++i)
+                    if (__any(!(x[i] < bar))) add(key(i));  // (a NaN is seen as -inf)
                 least = lane_key(list, a.top - 1);
             }
         }
         // ---- the sums
-        float y[kLaneValues], ref = big;
+        float m = big;
         if constexpr (CAP) {
-            ref = -INFINITY;
+            float most = 0.f;
 #pragma unroll
-            for (int i = 0; i < kLaneValues; ++i) {
-                y[i] = capped(x[i], a.softcap, inv);
-                ref = fmaxf(ref, y[i]);
+            for (int i = 0; i < kLaneValues; ++i) x[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < kLaneValues; ++i) most = fmaxf(most, fabsf(x[i]));
+            m *= inv;
+            if (__any(!(most < 0.35f))) {
+                m = tanh_of<false>(m);
+#pragma unroll
+                for (int i = 0; i < kLaneValues; ++i) x[i] = tanh_of<false>(x[i]);
+            } else {
+                m = tanh_of<true>(m);
+#pragma unroll
+                for (int i = 0; i < kLaneValues; ++i) x[i] = tanh_of<true>(x[i]);
             }
         }
-        const float m = ref;
-        ref = ref == -INFINITY ? 0.f : ref;
-        float rest = 0.f, all = 0.f, ent = 0.f;
+        const float ref = m == -INFINITY ? 0.f : m;
+        float rest = 0.f, ent = 0.f;
+        int equal = 0;  // to the largest one
 #pragma unroll
         for (int i = 0; i < kLaneValues; ++i) {
-            const float t = ((CAP ? y[i] : x[i]) - ref) * unit, p = __builtin_amdgcn_exp2f(t);
-            all += p;
+            const float t = (x[i] - ref) * unit, p = __builtin_amdgcn_exp2f(t);
             rest += t == 0.f ? 0.f : p;
+            equal += t == 0.f;
             ent -= p * fmaxf(t, -16384.0f);
         }
-        rest += m == -INFINITY ? 0.f : rintf(all - rest) - 1.0f;  // the equals of the largest one
+        rest += m == -INFINITY ? 0.f : (float)(equal - 1);
         sums = merge(sums, Sums{m, rest, ent}, unit);
     }
     if (part == a.parts - 1 && wave == 0) few(tail, a.vocab);
 
-    // ---- the lanes' sums, then the wavefronts'
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) sums = merge(sums, shuffled(sums, k), unit);
-    __shared__ Sums s_sums[kLogitWaves];
-    __shared__ rank_t s_list[kLogitWaves][64];
-    if (lane == 0) s_sums[wave] = sums;
-    if (a.top) s_list[wave][lane] = list;
-    __syncthreads();
-    sums = s_sums[0];
-#pragma unroll
-    for (int w = 1; w < kLogitWaves; ++w) sums = merge(sums, s_sums[w], unit);
-    if (a.top && wave == 0) {
-#pragma unroll
-        for (int w = 1; w < kLogitWaves; ++w) list = joined(list, s_list[w][lane], lane);
-    }
+    join_waves(a, unit, wave, lane, sums, list);
     if (a.parts == 1) {
         finish<BF>(a, row, sums, list);
         return;
@@ -278,7 +330,7 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = blockIdx.x, words = part_words(a.top);
     const float* in = a.work + row * a.parts * words;
-    const float unit = a.scale * kInvLog2;
+    const float unit = a.scale * kInvLog2 * (a.softcap > 0.f ? a.softcap : 1.0f);
     Sums sums = {-INFINITY, 0.f, 0.f};
     if ((int)threadIdx.x < a.parts) {
         const float* p = in + threadIdx.x * words;
@@ -291,27 +343,14 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = p0 + i * kLogitWaves;
-                k[i] = p < a.parts && lane < a.top ? reinterpret_cast<const rank_t*>(in + p * words + 4)[lane] : 0;
+                k[i] = p < a.parts && 63 - lane < a.top ? reinterpret_cast<const rank_t*>(in + p * words + 4)[63 - lane] : 0;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (lane_key(k[i], 0) > lane_key(list, a.top - 1)) list = joined(list, k[i], lane);
+                if (lane_key(k[i], 63) > lane_key(list, a.top - 1)) list = joined(list, k[i], lane);
         }
     }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) sums = merge(sums, shuffled(sums, k), unit);
-    __shared__ Sums s_sums[kLogitWaves];
-    __shared__ rank_t s_list[kLogitWaves][64];
-    if (lane == 0) s_sums[wave] = sums;
-    if (a.top) s_list[wave][lane] = list;
-    __syncthreads();
-    sums = s_sums[0];
-#pragma unroll
-    for (int w = 1; w < kLogitWaves; ++w) sums = merge(sums, s_sums[w], unit);
-    if (a.top && wave == 0) {
-#pragma unroll
-        for (int w = 1; w < kLogitWaves; ++w) list = joined(list, s_list[w][lane], lane);
-    }
+    join_waves(a, unit, wave, lane, sums, list);
     finish<BF>(a, row, sums, list);
 }
 
