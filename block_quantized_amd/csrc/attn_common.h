@@ -190,8 +190,8 @@ struct TreeRow {
 __device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const TileAt& t, int mt) {
     const int64_t row = t.row + mt;
     const int32_t d = a.depth[row];
-    // (no depth is trusted further than that it is a number: positions stay below 2^31)
-    return TreeRow{a.tree + row * a.words, a.depth + (t.row - t.first), t.base + min(max(d, 0), t.n)};
+    // (held to what a tree's can be: positions stay below kv, as the tiles' bounds take them)
+    return TreeRow{a.tree + row * a.words, a.depth + (t.row - t.first), t.base + min(max(d, 0), t.n - 1)};
 }
 // Which of the keys kb .. kb + 63 the row sees, window and prefix apart: those
 // before the new tokens, and its own of these.
@@ -206,7 +206,7 @@ __device__ __forceinline__ uint64_t tree_bits(const AttnArgs& a, const TileAt& t
 // The position of key j.
 __device__ __forceinline__ int tree_place(const TileAt& t, const TreeRow& r, int j) {
     const int i = j - t.base;  // (j is below 2^30, the base above -2^23)
-    return i < 0 || i >= t.n ? j : t.base + min(max(r.depth[i], 0), t.n);
+    return i < 0 || i >= t.n ? j : t.base + min(max(r.depth[i], 0), t.n - 1);
 }
 
 // A work item: a row tile of a sequence, and a part of the keys it sees.

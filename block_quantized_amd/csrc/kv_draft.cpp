@@ -94,11 +94,10 @@ int qmm_kv_compact(const qmm_kv_cache* caches, int count, const int32_t* table, 
     int rc;
     if ((rc = check_layers(caches, count))) return rc;
     const qmm_kv_cache& c = caches[0];
-    if (n_seqs <= 0 || n_seqs > kMaxSeqs || table_width <= 0 || width <= 0) return QMM_ERR_SHAPE;
+    if (n_seqs <= 0 || n_seqs > kMaxSeqs || table_width <= 0 || width < 0) return QMM_ERR_SHAPE;
     if ((int64_t)table_width * c.page_size > kMaxLength || width > kMaxLength) return QMM_ERR_SHAPE;
-    if ((rc = check_ptr(table, 4)) || (rc = check_ptr(first, 4)) || (rc = check_ptr(keep, 4)) ||
-        (rc = check_ptr(n_keep, 4)))
-        return rc;
+    if ((rc = check_ptr(table, 4)) || (rc = check_ptr(first, 4)) || (rc = check_ptr(n_keep, 4))) return rc;
+    if (width && (rc = check_ptr(keep, 4))) return rc;
     if (reinterpret_cast<uintptr_t>(kv_len) & 3) return QMM_ERR_ALIGN;
     if (kv_len && (kv_len == first || kv_len == n_keep)) return QMM_ERR_UNSUPPORTED;  // they are read while it is written
     if ((int64_t)n_seqs * c.n_kv >= int64_t(1) << 23) return QMM_ERR_SHAPE;

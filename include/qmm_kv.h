@@ -185,7 +185,7 @@ int qmm_attn_choice(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int xt
  * none.  It stands at position kv_len - n + depth[r]. */
 typedef struct {
     uint64_t* seen;  /* device, n_tokens x words, 16-byte aligned        */
-    int32_t* depth;  /* device, n_tokens                                 */
+    int32_t* depth;  /* device, n_tokens: 0 .. n - 1 (held to that)      */
     int32_t words;   /* 1 .. 16: room for 64 * words new tokens of a
                         sequence                                         */
 } qmm_kv_tree;
@@ -209,9 +209,11 @@ int qmm_kv_tree_build(const qmm_kv_batch* batch, const int32_t* parents, const q
  * slopes, and key j < kv_len is visible if
  *   ((j < kv_len - n or the row sees that new token)
  *    and (window == 0 or p - p_j < window))  or  j < prefix[s].
- * Keys and values of all new tokens have to be finite.  Everything else is as
- * in qmm_attn, the workspace (qmm_attn_tree_work) too.  No read leaves the
- * buffers for any contents of the tree. */
+ * Keys and values of all new tokens have to be finite.  opts->algo: 0 chosen by
+ * the sizes, 1 split kernels, 2 the kernels for more rows (tiles of 32 or 64; over
+ * Q8_0 rows only for heads of 64 and 128, else the split kernels).  Everything
+ * else is as in qmm_attn, the workspace (qmm_attn_tree_work) too.  No read leaves
+ * the buffers for any contents of the tree. */
 int qmm_attn_tree(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_kv_tree* tree, const qmm_attn_opts* opts,
                   int xtype, const void* q, int64_t ldq, int n_q, void* out, void* work, size_t work_bytes, void* stream);
 
@@ -226,7 +228,8 @@ size_t qmm_attn_tree_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, 
  *            is left out
  *   rows   : device, n: tokens of the page that are copied (held to [0,
  *            page_size]); NULL: all.  What lies behind stays as it is
- * No page may be in dst twice, or in src and dst of different pairs. */
+ * No page may be in dst twice, or in src and dst of different pairs.  At most 2^23
+ * pieces of 16 KiB of a page's keys (QMM_ERR_SHAPE otherwise). */
 int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const int32_t* dst, const int32_t* rows,
                 int64_t n, void* stream);
 
@@ -237,7 +240,7 @@ int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const
  *   table  : device, n_seqs x table_width pages, as in qmm_kv_batch
  *   first  : device, n_seqs
  *   keep   : device, n_seqs x width: rising in each sequence, so that
- *            keep[s][i] >= first[s] + i
+ *            keep[s][i] >= first[s] + i; not read where width is 0
  *   n_keep : device, n_seqs (held to [0, width])
  *   kv_len : device, n_seqs, written with first[s] + n_keep[s]; or NULL.  None of
  *            the inputs
