@@ -86,11 +86,11 @@ __device__ __forceinline__ float dpp(float x) {
 
 // Two fp16 parts of d c / 128 for pairs of int8 codes c and scales d: the product
 // rounded, and what that leaves off, which has no more bits than fp16 holds, so
-// that the parts are exact above its smallest step.  The codes lie in the low
-// bytes of 16 bits each (0x4800 | u is 8 + u / 128; with u = c + 128 9 less is c / 128).
-__device__ __forceinline__ void scaled_codes(uint32_t bytes, half2v d, uint32_t (&part)[2]) {
+// that the parts are exact above its smallest step.  `eights`: 0x4800 | c + 128 of
+// each, which is 9 + c / 128.
+__device__ __forceinline__ void scaled_codes(uint32_t eights, half2v d, uint32_t (&part)[2]) {
     const half2v nine = {(_Float16)9.0f, (_Float16)9.0f};
-    const half2v c = __builtin_bit_cast(half2v, bytes ^ 0x48804880u) - nine, hi = c * d;
+    const half2v c = __builtin_bit_cast(half2v, eights) - nine, hi = c * d;
     part[0] = __builtin_bit_cast(uint32_t, hi);
     part[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, d, -hi));
 }

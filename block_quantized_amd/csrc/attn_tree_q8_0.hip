@@ -34,6 +34,8 @@ namespace {
 
 constexpr int kTreeWaves = 4, kRows = 32;
 
+typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), c, 0, 0, 0);
 }
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
 
     // ---- the queries, as B operands in LDS: lane (r, h) holds eight values of
     // each step, 2 further on in the blocks whose codes are read from the third on
-    float qs;  // what a score is multiplied by
+    float qs;  // what a score is multiplied by, positive
     {
         const int64_t base = (int64_t)(at.row + mt) * a.ldq + (int64_t)head * D;
         auto shift = [](int s) { return s / 2 % 2 == 0 ? 2 : 0; };
@@ -134,8 +136,8 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
         frexpf(big, &ex);
         ex = min(max(ex, -110), 126);  // an all-zero row: any finite scale does
         constexpr int TOP = 14;
-        const float up = ldexpf(1.0f, TOP - ex);
-        qs = ldexpf(1.0f, ex - TOP) * a.scale;
+        const float up = copysignf(ldexpf(1.0f, TOP - ex), a.scale);  // the sign of the scale goes to the queries
+        qs = ldexpf(1.0f, ex - TOP) * fabsf(a.scale);
         // a wave writes every fourth step
         for (int s = wave; s < STEPS; s += kTreeWaves) {
             u4v q[QP];
@@ -154,6 +156,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
     __syncthreads();
     const bool capped = a.softcap > 0.f;
     if (!capped) qs *= kLog2e;
+    qs = fmaxf(qs, 0x1p-120f);  // never 0: masked scores stay -inf times it
     const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
     const int reach = a.window > 0 ? a.window : INT32_MAX;
 
@@ -171,17 +174,24 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
     // key i of the lane's scores, in the tile
     auto key_of = [&](int i) { return 8 * (i >> 2) + 4 * h + (i & 3); };
 
-    // ---- one tile's scores to P: sc in, p out; raises the running maximum where needed
+    float one = 1.0f;
+    asm("" : "+v"(one));  // (a product with it and a difference are one instruction on mixed types, if it is no constant)
+    // ---- one tile's scores to P: products in, p out; raises the running maximum where needed
     auto soften = [&](float (&sc)[16]) {
+        float f = qs;
         if (!now.whole && capped) {  // the scores of masked keys may be anything
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = kept(i >> 3, now.kb + key_of(i)) ? sc[i] : 0.f;
         }
-        if (capped) cap_scores(sc, 1.0f, a.softcap);
+        if (capped) {
+            cap_scores(sc, f, a.softcap);
+            f = 1.0f;
+        }
         auto place_of = [&](int key) { return now.whole ? key : tree_place(at, tree, key); };
         if (a.slopes) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] -= slope * fabsf((float)(tree.pos - place_of(now.kb + key_of(i))));
+            for (int i = 0; i < 16; ++i) sc[i] = sc[i] * f - slope * fabsf((float)(tree.pos - place_of(now.kb + key_of(i))));
+            f = 1.0f;
         }
         if (!now.whole) {
             const uint32_t bits = (uint32_t)(tree_bits(a, at, tree, now.kb) >> (4 * h));
@@ -196,8 +206,8 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
         float big = sc[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) big = fmaxf(big, sc[i]);
-        if (__any(big > mx + kSlack)) {
-            big = fmaxf(big, __shfl_xor(big, 32));
+        if (__any(big * f > mx + kSlack)) {
+            big = fmaxf(big, __shfl_xor(big, 32)) * f;
             const float top = fmaxf(mx, big), ref = top == -INFINITY ? 0.f : top;
             const float down = __builtin_amdgcn_exp2f(mx - ref);  // 0 from -inf
             mx = top;
@@ -208,18 +218,23 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            sc[i] = __builtin_amdgcn_exp2f(sc[i] - mref);
+            sc[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], f, -mref));
             l += sc[i];
         }
     };
     // P of step kk as B operands
+    static_assert(PP == 2, "two parts of P");
     auto p_operand = [&](const float (&sc)[16], int kk, u4v (&pf)[PP]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t part[PP];
-            split_pair<false, PP>(sc[8 * kk + 2 * i], sc[8 * kk + 2 * i + 1], part);
-#pragma unroll
-            for (int k = 0; k < PP; ++k) pf[k][i] = part[k];
+            // the value rounded, and what that leaves, rounded
+            const float x = sc[8 * kk + 2 * i], y = sc[8 * kk + 2 * i + 1];
+            half2v hi = {(_Float16)x, (_Float16)y}, lo;
+            uint32_t w = __builtin_bit_cast(uint32_t, hi);
+            asm("" : "+v"(w));
+            hi = __builtin_bit_cast(half2v, w);
+            lo.x = (_Float16)fmaf(x, one, -(float)hi.x), lo.y = (_Float16)fmaf(y, one, -(float)hi.y);
+            pf[0][i] = w, pf[1][i] = __builtin_bit_cast(uint32_t, lo);
         }
     };
 
@@ -342,7 +357,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[i] = fmaf(acc[(NB & 1) ^ 1][i], d[i / 4][i % 4], sc[i]) * qs;
+                for (int i = 0; i < 16; ++i) sc[i] = fmaf(acc[(NB & 1) ^ 1][i], d[i / 4][i % 4], sc[i]);
             }
             soften(sc);
             // ---- O^T += V^T P^T
@@ -395,8 +410,8 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint8_t* p = v + (8 * (j >> 1) + 2 * (j & 1)) * RB;
-                        x.w[j] = (uint32_t)*reinterpret_cast<const uint16_t*>(p) |
-                                 (uint32_t)*reinterpret_cast<const uint16_t*>(p + RB) << 16;
+                        const us2 two = {*reinterpret_cast<const uint16_t*>(p), *reinterpret_cast<const uint16_t*>(p + RB)};
+                        x.w[j] = __builtin_bit_cast(uint32_t, two);
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -404,14 +419,16 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
                 };
                 auto operand = [&](const Group& x, u4v (&vf)[2][AP]) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w = x.w[j] ^ 0x80808080u;
+                        const half2v d = __builtin_bit_cast(half2v, (uint32_t)(j & 1 ? x.d[j >> 1].y : x.d[j >> 1].x));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             uint32_t part[2];
-                            scaled_codes(__builtin_amdgcn_perm(0, x.w[j], 0x0C020C00u + 0x00010001u * e),
-                                         __builtin_bit_cast(half2v, (uint32_t)(j & 1 ? x.d[j >> 1].y : x.d[j >> 1].x)), part);
+                            scaled_codes(__builtin_amdgcn_perm(0x48484848u, w, 0x04020400u + 0x00010001u * e), d, part);
                             vf[e][0][j] = part[0], vf[e][AP - 1][j] = part[1];
                         }
+                    }
                 };
                 Group gr[2];
                 u4v vf[2][2][AP], pf[2][PP];
