@@ -19,14 +19,16 @@
 // (scaled_codes), times a power of two for each 32 values that keeps the largest
 // so far below 2^15; queries and P in 16-bit parts as in the tile kernels.
 //
-// Bound: two waves a SIMD, whose vector work (some 650 instructions a tile) and
-// products (40, 1280 cycles) overlap in part, beside the reading.  One sequence of
-// 295k keys, 8 heads of 128 (642 MB; read alone 117 us): 32 fp32 rows a head 187 us,
-// 64 (two row tiles) 312.  With nothing multiplied the former takes 147 us, with
-// nothing loaded 140.  The tile kernels in this form (64 rows staged in LDS, a half of
-// the keys each) took 290 and 345 us, the split kernels 250 and 430.  Operands read from
-// LDS a step ahead and converted between the products: 200 -> 187 us; loads a whole
-// tile ahead instead of half a one: no change.
+// Bound: two waves a SIMD, whose vector work (some 590 instructions a tile, 2400
+// cycles), LDS reads and products (40, 1280 cycles) overlap in part, beside the reading.
+// One sequence of 295k keys, 8 heads of 128 (642 MB; read alone 117 us): 32 fp32 rows a
+// head 183 us, 64 (two row tiles) 310.  With nothing multiplied the former took 147 us,
+// with nothing loaded 140 (125 now).  The tile kernels in this form (64 rows staged in
+// LDS, a half of the keys each) took 290 and 345 us, the split kernels 250 and 430.
+// Operands read from LDS a step ahead and converted between the products: 200 -> 187 us.
+// No change (2%): loads a whole tile ahead instead of half a one, loads straight to LDS,
+// non-temporal ones, every load of a tile unconditional.  More rows a wave, which would
+// unpack less often, do not fit: 253 registers.
 #include "attn_common.h"
 
 namespace qmm {

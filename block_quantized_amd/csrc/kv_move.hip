@@ -12,6 +12,9 @@ constexpr int kCopyBytes = 1 << 14;  // of a page that a workgroup takes: four 1
 // blockIdx.x: a piece of a page and its pair, blockIdx.y: the keys or values of
 // a layer.  PART: only the first rows of each head, so a lane looks where in its
 // head it stands; the last 16 bytes of them may be cut (rows are even in size).
+// Bound: reading and writing, each once.  130 pages of 32 tokens, 8 heads of 128 in
+// fp16, 32 layers (545 MB): 210 us, 5.2 TB/s, a large copy's rate.  One page of 16
+// layers: latency, 3.5 us.
 template <bool PART>
 __global__ __launch_bounds__(256) void kv_copy_kernel(LayerArgs l, CopyArgs a, int pieces) {
     const int64_t pair = blockIdx.x / pieces;
@@ -58,6 +61,11 @@ using Unit = std::conditional_t<RB % 16 == 0, u4v,
 // old one, and every later row's old place behind all of a chunk's new ones: so
 // a chunk is read whole before any of it is written, and chunks in their order
 // read nothing that was overwritten.
+// Bound: reading and writing, each once, where rows are many: 8 sequences keeping
+// 1900 rows of 256 bytes of 8 heads in 16 layers (788 MB moved) in 340 us, 4.6 TB/s of
+// the 5.1 of a large copy; a workgroup's next places are looked up while its rows are
+// on their way (390 us without).  Eight units a lane instead of four: no change.  One
+// path of 5 tokens in 32 layers: latency, 3.7 us.
 template <int RB>
 __global__ __launch_bounds__(256) void kv_compact_kernel(LayerArgs l, CompactArgs a) {
     using U = Unit<RB>;
