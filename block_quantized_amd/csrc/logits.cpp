@@ -1,5 +1,6 @@
 // logits.cpp — the C ABI of qmm_logits.h: argument checks and how rows are
 // divided, then the launch.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -23,6 +24,8 @@ int check_sizes(int xtype, int64_t rows, int64_t vocab, int top) {
     if (top < 0 || top > kMaxTop || top > vocab) return QMM_ERR_SHAPE;
     return QMM_OK;
 }
+
+bool held(double x) { return x >= FLT_MIN && 2 * x <= FLT_MAX; }  // in fp32, also times log2 e
 
 int check_array(const void* p) {
     if (!p) return QMM_ERR_NULL;
@@ -60,6 +63,8 @@ int qmm_logprobs(int xtype, const void* logits, int64_t ld, int64_t rows, int64_
     if (reinterpret_cast<uintptr_t>(logits) & (xtype == QMM_BF16 ? 1 : 3)) return QMM_ERR_ALIGN;
     if (ld < vocab || ld > INT64_MAX / 8 / rows) return QMM_ERR_SHAPE;
     if (!isfinite(scale) || scale <= 0 || !isfinite(softcap) || softcap < 0) return QMM_ERR_UNSUPPORTED;
+    const double cap = softcap > 0 ? softcap : 1.0;  // what the kernels multiply by
+    if (!held(scale) || !held(scale * cap) || 1.0 / cap > FLT_MAX) return QMM_ERR_UNSUPPORTED;
     if (n_tokens < 0 || n_tokens > 1 << 16) return QMM_ERR_SHAPE;
     if (n_tokens && ((rc = check_array(tokens)) || (rc = check_array(logp)))) return rc;
     if (n_top && ((rc = check_array(top_ids)) || (rc = check_array(top_logp)))) return rc;

@@ -30,7 +30,8 @@ extern "C" {
  *              aligned to their values
  *   rows, vocab : below 2^23; at most 2^28
  *   scale    : finite and positive (1 / temperature)
- *   softcap  : 0: none; else finite and positive
+ *   softcap  : 0: none; else finite and positive.  Scale and scale * softcap have
+ *              to be normal fp32 numbers below 2^127, 1 / softcap finite
  *   tokens, logp      : device, rows x n_tokens; not read where n_tokens is 0
  *   entropy           : device, rows; NULL: not wanted
  *   top_ids, top_logp : device, rows x n_top, n_top at most 64 and at most

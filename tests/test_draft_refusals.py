@@ -124,6 +124,12 @@ def test_logprobs(change, code):
     assert Q.qmm_logprobs(*a.values(), S) == code
 
 
+@pytest.mark.parametrize("scale,softcap", [(3e38, 0.0), (1e-39, 0.0), (1e30, 1e30), (1e-30, 1e-30), (1.0, 1e-39), (1.0, 1e-45)])
+def test_logprobs_numbers_that_fp32_does_not_hold(scale, softcap):
+    # scale log2 e, that times the cap, or 1 / cap would be infinite or no normal number
+    assert Q.qmm_logprobs(F32, A, 100, 3, 100, scale, softcap, A, 2, A, A, 5, A, A, A, 1 << 40, S) == Q.QMM_ERR_UNSUPPORTED
+
+
 def test_logprobs_work():
     assert Q.qmm_logprobs_work(F32, 1, 8185, 5) == 0  # one turn of a workgroup
     one = Q.qmm_logprobs_work(F32, 1, 128256, 20)
