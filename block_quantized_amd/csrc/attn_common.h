@@ -250,6 +250,17 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) all += __shfl_xor(all, k);
         chunk = max(a.least, (int)fmin(all / (double)a.splits, 1e9) + 1);
+        if constexpr (TREE) {
+            // `fit` (of 64 sequences at most): no more items than splits, if that can be.  Parts are cut to whole numbers a row tile, so equal ones of
+            // that size may be more: the chunk grows by a sixteenth until they fit, or no row tile is cut any more.
+            for (int i = 0; a.fit && i < 64; ++i) {
+                unsigned items = keys ? tiles * ((keys - 1) / chunk + 1) : tiles;
+#pragma unroll
+                for (int k = 1; k < 64; k <<= 1) items += (unsigned)__shfl_xor((int)items, k);
+                if (items <= (unsigned)a.splits || !__any(keys > chunk)) break;
+                chunk += (chunk >> 4) + 1;
+            }
+        }
     }
     int base = 0;
     for (int s0 = 0; s0 < n; s0 += 64) {

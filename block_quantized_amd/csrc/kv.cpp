@@ -15,6 +15,7 @@ namespace {
 // How qmm_attn divides its work.
 struct Plan {
     int algo, chunk, chunks, shift, splits, least, slots, rows;
+    bool fit;  // the splits are as many items as run at once
     int64_t items, parts;
 };
 
@@ -118,13 +119,19 @@ Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts
     if (p.algo == 1) {
         s = split_parts(c, tiles, heads, keys);
     } else {
-        // As many workgroups as run at once (two a CU, one of eight waves), a row tile's parts being some half more
-        // than the whole ones; twice as many where sequences are long and uneven (Q8_0, 128 values, above 4000 keys: 10%
-        // faster; one sequence of 7930: 50 us against 62).  Up to 512 keys the join would cost more than it saves.
+        // As many workgroups as run at once (two a CU, one of eight waves), which the kernels fit the parts into (those of
+        // more than 64 sequences by their mean: a row tile's parts are some half more than the whole ones).  Twice as many would end more evenly but begin and
+        // are joined as often again (Q8_0, 8 heads of 128, us with 512, 1024: 32 sequences of 6275 to 12287 keys, two row
+        // tiles each, 333, 345; 8 of 11459 to 20000, one each, 89, 95; 6 of 5157 to 9000, three each, 85, 89).  By
+        // the mean and an upper bound of row tiles, as the split kernels, half of the places stay empty where each sequence
+        // has one (16 drafts, fp32 over bf16, 16 sequences of 8000: 182 us, 142 so).  Up to 512 keys the join would cost
+        // more than it saves.
         const bool eight = p.rows == 64 && (c->head_dim > 128 || (c->type == QMM_BF16 && xtype == QMM_F32));
-        const int64_t run = eight ? 256 : q8 && c->head_dim == 128 && keys > 4000 && b->n_seqs > 1 ? 1024 : 512;
-        s = up_div(run, heads) - tiles / 2;
-        if (keys <= 512 || s <= tiles / 2) s = 0;
+        const int64_t run = eight ? 256 : 512;
+        const int64_t mean = up_div(each, int64_t(1) << p.shift) * b->n_seqs;  // row tiles if sequences are alike
+        p.fit = b->n_seqs <= 64;
+        s = run / heads;
+        s = keys <= 512 || s <= mean ? 0 : p.fit ? s : s - mean / 2;
     }
     if (s > most) s = most;
     p.splits = keys > 32 * p.least ? (int)s : 0;
@@ -246,6 +253,7 @@ int attend(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const qmm_kv_tr
         a.depth = tree->depth;
         a.words = tree->words;
         a.tile_rows = p.rows;
+        a.fit = p.fit;
     }
     return hip_status(launch_attn(p.algo, cache->type, cache->head_dim, xtype, a, static_cast<hipStream_t>(stream)));
 }

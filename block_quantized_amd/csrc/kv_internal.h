@@ -58,6 +58,7 @@ struct AttnArgs {
     const int32_t* depth;
     int32_t words;
     int32_t tile_rows;  // of the tile kernels: 32, 64 or 128
+    int32_t fit;        // splits are the items that run at once (64 sequences at most)
 };
 
 // What builds a tree from its tokens' parents.
