@@ -158,3 +158,16 @@ def test_many_sequences(cache, n_tokens):
     parents = trees(g, case[0].new, 6)
     for algo in (0, 1, 2):
         run(case, parents, q, R.F32, 1, 64, algo)
+
+
+@pytest.mark.parametrize("cache,dim", [(R.Q8, 64), (R.Q8, 128), (R.F16, 128), (R.BF16, 256)])
+@pytest.mark.parametrize("n_kv,lens,new", [
+    (32, (1900, 700, 1300), (9, 5, 12)),                                    # 16 (8) places, parts to grow until they fit
+    (8, (2100, 600, 900, 1500, 1, 0, 700, 40), (16, 8, 0, 9, 1, 0, 3, 20)),  # sequences without tokens and without old keys among them
+    (1, tuple(520 + 13 * (7 * i % 37) for i in range(70)), (1, 2) * 35),     # more sequences than a wavefront looks through at once
+    (2, tuple(600 + 9 * (5 * i % 61) for i in range(64)), (3,) * 64)])       # as many as that
+def test_divisions(cache, dim, n_kv, lens, new):
+    g = synth.rng(n_kv + dim)
+    case = setup(g, [(n, n + m) for n, m in zip(new, lens)], 64, cache, n_kv, dim)
+    q = R.as_type(synth.normal_f32(g, (case[0].N, n_kv * 2, dim)), R.F32)
+    run(case, trees(g, case[0].new, 5), q, R.F32, n_kv, dim, 2)
