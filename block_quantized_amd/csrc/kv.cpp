@@ -81,19 +81,20 @@ int64_t row_tiles(const qmm_kv_batch* b, int n_kv, int G, int rows) {
     return up_div(each, int64_t(1) << tile_tokens(rows, chunk, each)) * b->n_seqs * n_kv * up_div(G, chunk);
 }
 
-// Trees of new tokens have some rows a sequence, over long caches: 2 to 100
-// tokens of 1 to 32 heads a key-value head.  Split kernels take 16 of them, the
-// kernels of Q8_0 rows 32, the tile kernels 32 or 64 (heads above 128, which stage
-// 8 keys a wave: 64).  In units of 1000 products of a row tile with 32 keys of 64
-// values, their times over 180 drawn sizes are some 12 us (17 for wide heads) and 0.9
-// us a unit, 3 us more and 0.9 a unit (of half as many), 1 us more and 1.7 a unit.
-// The choice by these costs 4 to 7% (geometric mean) against the better one of
-// each size.  us, split against the others: 8 drafts over 8000 keys, 32 sequences, 32
-// heads on 8 of 128, Q8_0 180, 155; the same bf16 over bf16 221, 160; 13 drafts over 130911
-// keys in fp16 193, 113; 26 over 3100, 12 sequences, 16 heads on 8 of 256, bf16 164, 59;
-// 12 over 2000 of 14 heads on 2 of 64, Q8_0 16.1, 17.5; 62 over 61, fp32 over fp16, 10.6, 15.4.
-// Heads of 96, 192 and 256 over Q8_0 stay with the split kernels (256, above 4000 keys:
-// half of the tile kernels' time), which is why those have no form for Q8_0 here.
+// Trees of new tokens have some rows a sequence, over long caches: 2 to 100 tokens of 1 to
+// 32 heads a key-value head.  Split kernels take 16 of them, the kernels of Q8_0 rows 32,
+// the tile kernels 32 or 64 (heads above 128, which stage 8 keys a wave: 64).  In units of
+// 1000 products of a row tile with 32 keys of 64 values, their times over 180 drawn sizes
+// are some 12 us (17 for wide heads) and 0.9 us a unit, 3 us more and 0.9 a unit (of half
+// as many), 1 us more and 1.7 a unit (heads of 64) or 0.6 (wider ones).  The choice by
+// these costs 0.4% (Q8_0) and 3% (geometric mean) against the better one of each of 126
+// other sizes.  us, split against the others: 8 drafts over 8000 keys, 32 sequences, 32
+// heads on 8 of 128, Q8_0 180, 155; the same bf16 over bf16 221, 160; 13 drafts over
+// 130911 keys in fp16 193, 113; 26 over 3100, 12 sequences, 16 heads on 8 of 256, bf16
+// 164, 59; 12 over 2000 of 14 heads on 2 of 64, Q8_0 16.1, 17.5; 62 over 61, fp32 over
+// fp16, 10.6, 15.4. Heads of 96, 192 and 256 over Q8_0 stay with the split kernels (256,
+// above 4000 keys: half of the tile kernels' time), which is why those have no form for
+// Q8_0 here.
 Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts* o, int xtype, int n_q) {
     Plan p = {};
     const int G = n_q / c->n_kv;
@@ -104,7 +105,7 @@ Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts
     if (o->window > 0 && !o->prefix && o->window + each < keys) keys = o->window + each;
     const double unit = 1e-3 * (double)keys / 32 * (c->head_dim / 64.0);
     const double split = 0.9 * unit * (double)row_tiles(b, c->n_kv, G, kSplitRows);
-    const double other = (q8 ? 3.0 : 1.0) + (q8 ? 0.9 : 1.7) * unit * (double)row_tiles(b, c->n_kv, G, rows);
+    const double other = (q8 ? 3.0 : 1.0) + (q8 ? 0.9 : c->head_dim > 64 ? 0.6 : 1.7) * unit * (double)row_tiles(b, c->n_kv, G, rows);
     p.algo = only_split ? 1 : o->algo ? o->algo : other < split ? 2 : 1;
     p.rows = p.algo == 1 ? kSplitRows : rows;
     p.chunk = G < p.rows ? G : p.rows;
