@@ -195,12 +195,11 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         if constexpr (TREE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) place[i] = kb + 16 * (i >> 2) + 4 * g + (i & 3);
-            if (!whole) {
-                bits = tree_bits(a, at, tree, kb) >> (4 * g);
-                if (a.slopes || a.window > 0) {
+            if (!whole) bits = tree_bits(a, at, tree, kb) >> (4 * g);
+            // (a tile that a prefix makes whole may hold new tokens, too)
+            if (kb + 32 > at.base && (a.slopes || a.window > 0)) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) place[i] = tree_place(at, tree, place[i]);
-                }
+                for (int i = 0; i < 8; ++i) place[i] = tree_place(at, tree, place[i]);
             }
         }
         if (a.slopes) {

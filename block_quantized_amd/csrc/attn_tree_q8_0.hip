@@ -189,7 +189,8 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
             cap_scores(sc, f, a.softcap);
             f = 1.0f;
         }
-        auto place_of = [&](int key) { return now.whole ? key : tree_place(at, tree, key); };
+        // (a tile that a prefix makes whole may hold new tokens, too)
+        auto place_of = [&](int key) { return now.kb + 32 > at.base ? tree_place(at, tree, key) : key; };
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = sc[i] * f - slope * fabsf((float)(tree.pos - place_of(now.kb + key_of(i))));
