@@ -84,6 +84,16 @@ __device__ __forceinline__ float dpp(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
 }
 
+// The sum over a wavefront's lanes, all of them active: within each 16 by DPP.
+__device__ __forceinline__ int sum_lanes(int x) {
+    x += __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);   // lane ^ 1
+    x += __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);   // lane ^ 2
+    x += __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false);  // 7 - lane, of each 8
+    x += __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false);  // 15 - lane, of each 16
+    return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) + __builtin_amdgcn_readlane(x, 32) +
+           __builtin_amdgcn_readlane(x, 48);
+}
+
 // Two fp16 parts of d c / 128 for pairs of int8 codes c and scales d: the product
 // rounded, and what that leaves off, which has no more bits than fp16 holds, so
 // that the parts are exact above its smallest step.  `eights`: 0x4800 | c + 128 of
@@ -251,14 +261,23 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, Work& w, 
         for (int k = 1; k < 64; k <<= 1) all += __shfl_xor(all, k);
         chunk = max(a.least, (int)fmin(all / (double)a.splits, 1e9) + 1);
         if constexpr (TREE) {
-            // `fit` (of 64 sequences at most): no more items than splits, if that can be.  Parts are cut to whole numbers a row tile, so equal ones of
-            // that size may be more: the chunk grows by a sixteenth until they fit, or no row tile is cut any more.
-            for (int i = 0; a.fit && i < 64; ++i) {
-                unsigned items = keys ? tiles * ((keys - 1) / chunk + 1) : tiles;
-#pragma unroll
-                for (int k = 1; k < 64; k <<= 1) items += (unsigned)__shfl_xor((int)items, k);
-                if (items <= (unsigned)a.splits || !__any(keys > chunk)) break;
-                chunk += (chunk >> 4) + 1;
+            // `fit` (64 sequences at most): no more items than splits, if parts of up to twice the even share make it so:
+            // parts are cut to whole numbers a row tile, so equal ones of the share may be more.  Where they are too many
+            // also then, as behind a long sequence among row tiles that fill the places already, twice the share stays: no
+            // workgroup walks more, and the items beyond one a row tile are half of the splits at most.
+            auto fits = [&](unsigned size) {
+                return sum_lanes(keys ? tiles * ((keys - 1) / size + 1) : tiles) <= a.splits;
+            };
+            if (a.fit && !fits(chunk)) {
+                unsigned low = chunk, high = 2 * chunk;
+                for (int i = 0; i < 6 && high - low > 1; ++i) {  // to a 64th of the share
+                    const unsigned mid = low + (high - low) / 2;
+                    if (fits(mid))
+                        high = mid;
+                    else
+                        low = mid;
+                }
+                chunk = high;
             }
         }
     }

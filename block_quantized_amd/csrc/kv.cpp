@@ -130,9 +130,19 @@ Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts
         const bool eight = p.rows == 64 && (c->head_dim > 128 || (c->type == QMM_BF16 && xtype == QMM_F32));
         const int64_t run = eight ? 256 : 512;
         const int64_t mean = up_div(each, int64_t(1) << p.shift) * b->n_seqs;  // row tiles if sequences are alike
-        p.fit = b->n_seqs <= 64;
         s = run / heads;
-        s = keys <= 512 || s <= mean ? 0 : p.fit ? s : s - mean / 2;
+        if (keys <= 512) {
+            s = 0;
+        } else if (s > mean) {
+            p.fit = b->n_seqs <= 64;
+            s = p.fit ? s : s - mean / 2;
+        } else {
+            // Row tiles fill the places, but one sequence may be far longer than the others: parts of twice the even share
+            // cut nothing else (us without, with: 64 sequences of 8 drafts, one of 131072 keys, 63 of 1024, 32 heads on 8 of
+            // 128, Q8_0 2336, 170; bf16 over fp16 2364, 177).  All rows pay for the join that may follow (32 of 16 drafts, up
+            // to 12287 keys: 344, 349), so not below 4096 keys of 128 values, which one workgroup walks in some 75 us.
+            s = keys * c->head_dim >= 4096 * 128 && s >= 4 ? s / 2 : 0;
+        }
     }
     if (s > most) s = most;
     p.splits = keys > 32 * p.least ? (int)s : 0;
