@@ -334,12 +334,14 @@ def mul_mat(wtype: int, W, xq, M: int, N: int, K: int, algo: int = 0, stream=Non
 
 _torch = None  # torch, once a helper below has needed it
 _raw_stream = None  # device index -> handle of its current stream
+_forward_ad = None  # torch.autograd.forward_ad
 
 
 def _need_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _forward_ad
     if _torch is None:
         import torch
+        import torch.autograd.forward_ad as _forward_ad
         # a tenth of a microsecond instead of the two that a Stream object takes
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -508,7 +510,10 @@ def _xtype(what: str, dtype):
 
 
 def _no_grad(what: str, *tensors):
-    if _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    # (a dual tensor requires no gradient; outside of every dual level there is none)
+    if (_torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+            or getattr(_forward_ad, "_current_level", 0) >= 0
+            and any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors)):
         _refuse(QMM_ERR_UNSUPPORTED, f"{what}: no gradients are computed; detach the inputs or use torch.no_grad()")
 
 
@@ -519,7 +524,8 @@ def _new_out(x):
 def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=None, stream=None):
     """Stores k (rotated) and v (tokens, n_kv, head_dim) in the cache, and
     returns q (tokens, n_q, head_dim) rotated, in q_out if given.  No
-    gradients: inputs that require them are refused where torch records them."""
+    gradients: inputs that require them are refused where torch records them,
+    and inputs that carry a tangent."""
     torch = _torch or _need_torch()
     dev, N, D, dtype = cache.dev, batch.n_tokens, cache.head_dim, k.dtype
     same = batch.dev == dev and k.get_device() == dev and v.get_device() == dev and v.dtype == dtype
@@ -736,7 +742,8 @@ def logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, softcap: flo
     entropy of each row, and the top largest logits' ids and log probabilities
     (64 at most).  x = scale * softcap * tanh(logits / softcap).  What is not
     asked for is None.  No gradients: logits that require them are refused
-    where torch records them."""
+    where torch records them, and logits that carry a tangent.  At least one
+    row."""
     torch = _torch or _need_torch()
     if logits.dim() != 2:
         _refuse(QMM_ERR_SHAPE, "logprobs: logits have to be rows x vocab")
