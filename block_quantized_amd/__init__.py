@@ -657,7 +657,7 @@ def _attend(cache, batch, tree, opts, xtype, q, ldq, n_q, out, handle):
 
 class KVLayers:
     """The caches of a model's layers, of one geometry and on one GPU, for what
-    moves rows in all of them at once."""
+    moves rows in all of them at once; no array of them in another one."""
 
     def __init__(self, caches):
         self.caches = list(caches)
@@ -669,6 +669,10 @@ class KVLayers:
             _refuse(QMM_ERR_SHAPE, "KVLayers: the caches have to be of one geometry")
         if any(c.dev != f.dev for c in self.caches):
             _refuse(QMM_ERR_UNSUPPORTED, "KVLayers: the caches have to lie on one GPU")
+        # (rows that two workgroups move in place at once end anywhere)
+        size, at = f.k.numel() * f.k.element_size(), sorted([c.c.k for c in self.caches] + [c.c.v for c in self.caches])
+        if any(b - a < size for a, b in zip(at, at[1:])):
+            _refuse(QMM_ERR_UNSUPPORTED, "KVLayers: the caches' arrays must not overlap, and no cache be there twice")
         self.dev, self.n = f.dev, len(self.caches)
         self.c = (qmm_kv_cache * self.n)(*[c.c for c in self.caches])
 

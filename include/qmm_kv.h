@@ -223,7 +223,8 @@ size_t qmm_attn_tree_work(const qmm_kv_cache* cache, const qmm_kv_batch* batch, 
 
 /* Copies rows of pages, in the layers of a model at once: what a conversation
  * that goes on in two ways needs of the page they would both write to.
- *   caches : host array of count layers of the same geometry
+ *   caches : host array of count layers of the same geometry, whose arrays of
+ *            keys and values do not overlap
  *   src, dst : device, n page numbers each; a pair with one outside [0, n_pages)
  *            is left out
  *   rows   : device, n: tokens of the page that are copied (held to [0,
@@ -236,7 +237,8 @@ int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const
 /* Moves the rows that sequences keep to consecutive indexes, in place, in the
  * layers of a model at once: sequence s's token keep[s * width + i] goes to index
  * first[s] + i, for i < n_keep[s].  The rest of the cache stays as it is.
- *   caches : host array of count layers of the same geometry
+ *   caches : host array of count layers of the same geometry, whose arrays of
+ *            keys and values do not overlap
  *   table  : device, n_seqs x table_width pages, as in qmm_kv_batch
  *   first  : device, n_seqs
  *   keep   : device, n_seqs x width: rising in each sequence, so that
