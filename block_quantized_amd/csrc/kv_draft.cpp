@@ -22,6 +22,12 @@ int check_layers(const qmm_kv_cache* caches, int count) {
     return QMM_OK;
 }
 
+// Whether n of the values at a lie among m at b.
+bool meet(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * m && y < x + 4 * n;
+}
+
 template <typename F>
 int each_layers(const qmm_kv_cache* caches, int count, F launch) {
     for (int at = 0; at < count; at += kMaxLayers) {
@@ -99,7 +105,11 @@ int qmm_kv_compact(const qmm_kv_cache* caches, int count, const int32_t* table, 
     if ((rc = check_ptr(table, 4)) || (rc = check_ptr(first, 4)) || (rc = check_ptr(n_keep, 4))) return rc;
     if (width && (rc = check_ptr(keep, 4))) return rc;
     if (reinterpret_cast<uintptr_t>(kv_len) & 3) return QMM_ERR_ALIGN;
-    if (kv_len && (kv_len == first || kv_len == n_keep)) return QMM_ERR_UNSUPPORTED;  // they are read while it is written
+    // (the inputs are read while it is written)
+    if (kv_len && (meet(kv_len, n_seqs, first, n_seqs) || meet(kv_len, n_seqs, n_keep, n_seqs) ||
+                   meet(kv_len, n_seqs, keep, width ? (int64_t)n_seqs * width : 0) ||
+                   meet(kv_len, n_seqs, table, (int64_t)n_seqs * table_width)))
+        return QMM_ERR_UNSUPPORTED;
     if ((int64_t)n_seqs * c.n_kv >= int64_t(1) << 23) return QMM_ERR_SHAPE;
     CompactArgs a = {};
     a.table = table;

@@ -244,8 +244,8 @@ int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const
  *   keep   : device, n_seqs x width: rising in each sequence, so that
  *            keep[s][i] >= first[s] + i; not read where width is 0
  *   n_keep : device, n_seqs (held to [0, width])
- *   kv_len : device, n_seqs, written with first[s] + n_keep[s]; or NULL.  None of
- *            the inputs
+ *   kv_len : device, n_seqs, written with first[s] + n_keep[s]; or NULL.  It must
+ *            not overlap an input (QMM_ERR_UNSUPPORTED)
  * A token whose old or new place has no page is not moved.  Where keep does not
  * rise, what moves is undefined, but stays within the cache.  The rows that are
  * written must not lie in pages of other sequences too. */
