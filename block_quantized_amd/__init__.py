@@ -549,7 +549,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope=None, q_out=Non
             _refuse(QMM_ERR_SHAPE, "kv_append: pos has to name a position for every token")
     if not same:
         _refuse(QMM_ERR_UNSUPPORTED, "kv_append: tensors have to lie on one GPU and be of one type")
-    _no_grad("kv_append", k, v, q, q_out)
+    _no_grad("kv_append", k, v, q, q_out, cache.k, cache.v)
     xtype = _xtype("kv_append", dtype)
     if stream is not None or torch.cuda.current_device() != dev:
         handle, where = _elsewhere(dev, stream)
@@ -627,7 +627,7 @@ def attn(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0, wi
         _refuse(QMM_ERR_UNSUPPORTED, "attn: tensors have to lie on one GPU, and out be of q's type")
     if not 0 <= window < 1 << 31 or not 0 <= algo <= 2:  # ctypes would take their low 32 bits
         _refuse(QMM_ERR_UNSUPPORTED, "attn: window has to be 0 to 2^31 - 1, algo 0 to 2")
-    _no_grad("attn", q, slopes, out)
+    _no_grad("attn", q, slopes, out, cache.k, cache.v)
     xtype = _xtype("attn", dtype)
     opts = ctypes.byref(qmm_attn_opts(D ** -0.5 if scale is None else scale, softcap, window, algo, _ptr(slopes),
                                       _ptr(prefix)))
