@@ -572,9 +572,12 @@ def _append(cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, n_q, q_out, handl
 class KVTree:
     """The new tokens of a batch as trees of drafts: parents (int32, n_tokens)
     names each token's parent by its place among the new tokens of its
-    sequence, before its own; -1: none.  max_new: the most new tokens that a
-    sequence has (at most 1024; all of the batch's unless given).  pos (1 x
-    n_tokens) are the tokens' positions, for :class:`Rope`."""
+    sequence, before its own; -1: none.  max_new: the most new tokens that any
+    sequence has, at most 1024; all of the batch's unless given, so a batch of
+    more needs it.  It is not checked against the sequences, which lie on the
+    GPU: what one has beyond max_new rounded up to a multiple of 64 sees no new
+    token, not itself either, so that its results are not what they should be.
+    pos (1 x n_tokens) are the tokens' positions, for :class:`Rope`."""
 
     def __init__(self, batch: KVBatch, parents, max_new=None, stream=None):
         torch = _need_torch()
@@ -584,7 +587,7 @@ class KVTree:
             _refuse(QMM_ERR_UNSUPPORTED, "KVTree: parents have to lie on the batch's GPU")
         most = min(n, 1 << 30) if max_new is None else max_new
         if not 1 <= most <= 1024:
-            _refuse(QMM_ERR_SHAPE, "KVTree: max_new, the new tokens of a sequence, has to be 1 to 1024")
+            _refuse(QMM_ERR_SHAPE, "KVTree: max_new, the most new tokens of a sequence, has to be 1 to 1024 (given, where the batch has more)")
         self.dev, self.n_tokens, self.words = batch.dev, n, -(-most // 64)
         handle, where = _elsewhere(self.dev, stream)
         with where:
@@ -711,7 +714,8 @@ def kv_copy(layers: KVLayers, src, dst, rows=None, stream=None):
 def kv_compact(layers: KVLayers, table, first, keep, n_keep, kv_len=None, stream=None):
     """Moves the tokens keep[s, :n_keep[s]] (int32, rising) of every sequence to
     its indexes from first[s] on, in place in every layer, and writes the new
-    lengths first + n_keep to kv_len if given."""
+    lengths first + n_keep to kv_len if given.  Keys keep the rotation of the
+    positions they were appended with (see qmm_kv.h for dropping old tokens)."""
     if table.dim() != 2 or keep.dim() != 2:
         _refuse(QMM_ERR_SHAPE, "kv_compact: table and keep have to be n_seqs x width")
     n, width = keep.shape

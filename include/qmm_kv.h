@@ -246,6 +246,12 @@ int qmm_kv_copy(const qmm_kv_cache* caches, int count, const int32_t* src, const
  *   n_keep : device, n_seqs (held to [0, width])
  *   kv_len : device, n_seqs, written with first[s] + n_keep[s]; or NULL.  It must
  *            not overlap an input (QMM_ERR_UNSUPPORTED)
+ * Rows are moved as they are: a key keeps the rotation of the position at which
+ * it was appended, while windows, slopes and qmm_kv_append without pos go by the
+ * new index.  For the path that is kept of a tree the two are the same.  For what
+ * else is dropped, say the middle of a long conversation, they are not: there the
+ * program goes on numbering as its model should see it, by pos of qmm_kv_append,
+ * and a window or a slope counts the tokens that are left.
  * A token whose old or new place has no page is not moved.  Where keep does not
  * rise, what moves is undefined, but stays within the cache.  The rows that are
  * written must not lie in pages of other sequences too. */

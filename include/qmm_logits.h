@@ -28,11 +28,12 @@ extern "C" {
  *   xtype    : QMM_F32 or QMM_BF16, the type of the logits
  *   logits   : device, rows of vocab values, ld values apart (at least vocab);
  *              aligned to their values
- *   rows, vocab : below 2^23; at most 2^28
+ *   rows, vocab : 1 or more, below 2^23; at most 2^28
  *   scale    : finite and positive (1 / temperature)
  *   softcap  : 0: none; else finite and positive.  Scale and scale * softcap have
  *              to be normal fp32 numbers below 2^127, 1 / softcap finite
- *   tokens, logp      : device, rows x n_tokens; not read where n_tokens is 0
+ *   tokens, logp      : device, rows x n_tokens (at most 65536); not read where
+ *                       n_tokens is 0
  *   entropy           : device, rows; NULL: not wanted
  *   top_ids, top_logp : device, rows x n_top, n_top at most 64 and at most
  *                       vocab; not read where n_top is 0
