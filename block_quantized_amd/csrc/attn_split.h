@@ -89,6 +89,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
     const int low_last = a.window > 0 ? max(TREE ? at.kv : at.pos + at.tokens, 0) - a.window : INT32_MIN;
     // and up to here
     const int all_see = TREE ? at.base : at.pos + 1;
+    // or up to here by the prefix; new tokens of a tree are looked at one by one where slopes go by their positions
+    const int pre_see = TREE && a.slopes ? min(at.pre, at.base) : at.pre;
 
     // ---- where the wave's tiles lie.  Lane i holds the cache row of 16 keys:
     // half i % 2 of the i / 2-th tile from the last lookup on; -1: no page
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
         kb = 32 * (t < n_pre ? t : t - n_pre + w0);
         whole = r0[0] >= 0 && r0[1] >= 0 &&
-                ((kb + 32 <= at.pre) || (kb >= low_last && kb + 32 <= min(at.len, all_see)));
+                ((kb + 32 <= pre_see) || (kb >= low_last && kb + 32 <= min(at.len, all_see)));
     };
     // the first lookup is under way while the queries are prepared
     int t = t0 + wave;
@@ -195,11 +197,12 @@ __global__ __launch_bounds__(256, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnAr
         if constexpr (TREE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) place[i] = kb + 16 * (i >> 2) + 4 * g + (i & 3);
-            if (!whole) bits = tree_bits(a, at, tree, kb) >> (4 * g);
-            // (a tile that a prefix makes whole may hold new tokens, too)
-            if (kb + 32 > at.base && (a.slopes || a.window > 0)) {
+            if (!whole) {
+                bits = tree_bits(a, at, tree, kb) >> (4 * g);
+                if (a.slopes || a.window > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) place[i] = tree_place(at, tree, place[i]);
+                    for (int i = 0; i < 8; ++i) place[i] = tree_place(at, tree, place[i]);
+                }
             }
         }
         if (a.slopes) {

@@ -73,13 +73,15 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
     const int per = (n_tiles + w.splits - 1) / w.splits;
     const int t0 = w.split * per, t1 = min(n_tiles, t0 + per);
     const int low_last = a.window > 0 ? max(at.kv, 0) - a.window : INT32_MIN;  // every row sees keys from here
+    // or up to here by the prefix; new tokens are looked at one by one where slopes go by their positions
+    const int pre_see = a.slopes ? min(at.pre, at.base) : at.pre;
 
     // ---- where the wave's tiles lie, as in the split kernels
     int64_t my_row = -1;
     struct Where {
         int64_t r0[2];
         int kb;      // first key of the tile
-        bool whole;  // every row sees all of its keys
+        bool whole;  // every row sees all of its keys, which stand at their indexes
     };
     auto place = [&](int t) {
         Where x;
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
                                 (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_row >> 32), 2 * nth + u) << 32);
         x.kb = 32 * (t < n_pre ? t : t - n_pre + w0);
         x.whole = x.r0[0] >= 0 && x.r0[1] >= 0 &&
-                  ((x.kb + 32 <= at.pre) || (x.kb >= low_last && x.kb + 32 <= min(at.len, at.base)));
+                  ((x.kb + 32 <= pre_see) || (x.kb >= low_last && x.kb + 32 <= min(at.len, at.base)));
         return x;
     };
     int t = t0 + wave;
@@ -189,8 +191,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
             cap_scores(sc, f, a.softcap);
             f = 1.0f;
         }
-        // (a tile that a prefix makes whole may hold new tokens, too)
-        auto place_of = [&](int key) { return now.kb + 32 > at.base ? tree_place(at, tree, key) : key; };
+        auto place_of = [&](int key) { return now.whole ? key : tree_place(at, tree, key); };
         if (a.slopes) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = sc[i] * f - slope * fabsf((float)(tree.pos - place_of(now.kb + key_of(i))));
