@@ -510,10 +510,15 @@ def _xtype(what: str, dtype):
 
 
 def _no_grad(what: str, *tensors):
+    lost = False
+    if _torch.is_grad_enabled():
+        for t in tensors:  # (any() over them takes 0.2 us more)
+            if t is not None and t.requires_grad:
+                lost = True
     # (a dual tensor requires no gradient; outside of every dual level there is none)
-    if (_torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-            or getattr(_forward_ad, "_current_level", 0) >= 0
-            and any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors)):
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        lost = lost or any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    if lost:
         _refuse(QMM_ERR_UNSUPPORTED, f"{what}: no gradients are computed; detach the inputs or use torch.no_grad()")
 
 
