@@ -54,8 +54,10 @@
 // waves share the staging, so the bound is reading again.  13 tokens over 130911 keys
 // in fp16 (32 heads, of 128, on 8; bf16 queries; 537 MB): 103 us, 5.2 TB/s, and 6.6 for
 // the join.  12 sequences of 26 tokens over a window of 2048 keys (16 heads, of 256, on
-// 8; bf16, cap; 200 MB): 52 us and 5 for the join, 3.8 TB/s; at most 256 workgroups
-// run at once, one a CU, so that most sequences' keys are cut in two a head.  Tiles of 128 rows in this form did not fit the registers.
+// 8; bf16, cap; 200 MB): 51 us and 5 for the join, 3.9 TB/s; at most 256 workgroups
+// run at once, one a CU: eight sequences are cut in three a head, four in two, and the
+// longest part has 1.36 times the even share of keys.  Tiles of 128 rows in this form did
+// not fit the registers.
 #pragma once
 
 #include "attn_common.h"

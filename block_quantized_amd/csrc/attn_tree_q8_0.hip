@@ -28,7 +28,7 @@
 // Operands read from LDS a step ahead and converted between the products: 200 -> 187 us.
 // No change (2%): loads a whole tile ahead instead of half a one, loads straight to LDS,
 // non-temporal ones, every load of a tile unconditional.  More rows a wave, which would
-// unpack less often, do not fit: 253 registers.
+// unpack less often, do not fit beside another wave: 253 registers of 256.
 #include "attn_common.h"
 
 namespace qmm {
@@ -479,8 +479,7 @@ __global__ __launch_bounds__(256, 2) void attn_tree_kernel(AttnArgs a) {
 #pragma unroll
     for (int c = 0; c < PAIRS; ++c) {
         __syncthreads();
-        // rows 8 j + 4 h .. + 3 of both products: eight values one after another (16 rows: a block of 32 values)
-        // (16-bit rows: values 2 (8 j + 4 h) on; Q8_0 the same, the second block's rows from 16 on)
+        // rows 8 j + 4 h .. + 3 of both products: eight values one after another, from 2 (8 j + 4 h) on
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -25,7 +25,7 @@
 //
 // Bound: large calls by vector instructions (the vector unit is busy for 99% of the
 // time), 22 to 25 issue slots a value with a cap (8 of them the cap's polynomial, 4 the
-// exponential), some 15 without: 2048 rows of 151936 in bf16, cap, 8 largest, 622 MB, 211 us, 2.9 TB/s.
+// exponential), some 15 without: 2048 rows of 151936 in bf16, cap, 8 largest, 622 MB, 211 to 216 us, 2.9 TB/s.
 // 257 rows of 128256 in fp32, no cap, 4 tokens and 5 largest, 132 MB, 36 us with the
 // join (31 + 5): 3.7 TB/s; 49% of the vector unit's time, two waves a SIMD.  One row
 // of 128256, 20 largest: latency, 8.9 us and 4.4 for the join: loads, two sorts, the
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a) {
     };
     const int head = min(q0 * N - skew, a.vocab), tail = max(q1 * N - skew, head);
     if (part == 0 && wave == 0) few(0, head);
-    // (bf16: the next segment's loads go ahead of this one's arithmetic, 298 -> 281 us for 2048 rows of 151936 with a cap;
+    // (bf16: the next segment's loads go ahead of this one's arithmetic, 222 -> 215 us for 2048 rows of 151936 with a cap;
     // fp32 values stay in the registers they were loaded to, and the waves' number hides the loads: 36 us for 257 rows of
     // 128256, 39 with loads ahead)
     u4v w[LOADS];
