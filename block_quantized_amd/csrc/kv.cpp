@@ -140,8 +140,10 @@ Plan plan_tree(const qmm_kv_cache* c, const qmm_kv_batch* b, const qmm_attn_opts
             // Row tiles fill the places, but one sequence may be far longer than the others: parts of twice the even share
             // cut nothing else (us without, with: 64 sequences of 8 drafts, one of 131072 keys, 63 of 1024, 32 heads on 8 of
             // 128, Q8_0 2336, 170; bf16 over fp16 2364, 177).  All rows pay for the join that may follow (32 of 16 drafts, up
-            // to 12287 keys: 344, 349), so not below 4096 keys of 128 values, which one workgroup walks in some 75 us.
-            s = keys * c->head_dim >= 4096 * 128 && s >= 4 ? s / 2 : 0;
+            // to 12287 keys: 344, 349), so not below 4096 keys of 128 values, which one workgroup walks in 75 to 120 us; and
+            // every row has room in the workspace, so not from 16 times the places on, where the others' rows take
+            // long, too (32 x 512 workgroups of 64 rows of 128 values: 545 MB at most).
+            s = keys * c->head_dim >= 4096 * 128 && s >= 4 && mean <= 16 * s ? s / 2 : 0;
         }
     }
     if (s > most) s = most;

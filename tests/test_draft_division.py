@@ -19,3 +19,13 @@ def test_long_caches_can_be_cut(type, xtype, seqs, new):
                 assert Q.qmm_attn_tree_work(c, b, o, xtype, n_q) > 0
         b = Q.qmm_kv_batch(None, None, None, seqs, 2, seqs * new, 128)
         assert Q.qmm_attn_tree_work(c, b, o, xtype, 32) == 0
+
+
+@pytest.mark.parametrize("type", [Q.QMM_Q8_0, Q.QMM_F16, Q.QMM_BF16])
+def test_the_workspace_stays_small(type):
+    # every row has room in it, so batches of very many rows keep none for a long sequence
+    c = Q.qmm_kv_cache(None, None, type, 8, 128, 64, 1 << 24)
+    o = Q.qmm_attn_opts(0.1, 0.0, 0, 2, None, None)
+    for seqs in (64, 256, 1024, 4096, 65536):
+        b = Q.qmm_kv_batch(None, None, None, seqs, 2049, 8 * seqs, 131072)
+        assert Q.qmm_attn_tree_work(c, b, o, Q.QMM_BF16, 32) <= 300 << 20
